@@ -297,7 +297,7 @@ def _run_plain(s, c):
         if not c["ddm"]:
             return dw
         return dw, (s["w"][:, :, None] * s["dout"][:, None, :]).reshape(T * K, H)
-    out = s["base"].float()
+    out = s["base"].to(torch.float32, copy=True)
     if c["tokens"] <= 64:
         # few rows: every row's own matrices gathered
         a = s["ids"].clamp(min=0).long()
