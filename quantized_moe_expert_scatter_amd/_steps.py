@@ -1,0 +1,219 @@
+"""ctypes binding of the C ABI in include/moe_layer.h: the steps around the
+expert products (router, balance loss, gradients, per-request adapters).
+
+Every function keeps the C name and forwards to libmoe_prefill.so.  Tensors
+are the caller's, on the current HIP device; what the C call cannot see (a
+tensor's type, shape, strides and device) is checked here, and a bad one
+raises MoeError with the status the C call would give.  Work is enqueued on
+`stream`, by default torch's current stream; a tensor made on another stream
+must be ready on it, and one freed early must be kept until the work has run.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import _lib
+from ._lib import MoeError
+
+MOE_F32, MOE_BF16, MOE_F16 = 0, 1, 2
+MOE_ROUTE_RENORM = 1
+
+# every symbol include/moe_layer.h declares
+EXPORTS = ["moe_route", "moe_balance_bytes", "moe_route_balance", "moe_route_backward",
+           "moe_combine_backward", "moe_adapters_bytes", "moe_adapters"]
+
+
+class moe_adapter_set(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("n_adapter", ctypes.c_int), ("rank", ctypes.c_int),
+                ("n_in", ctypes.c_int), ("n_out", ctypes.c_int), ("a", ctypes.c_void_p),
+                ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("ranks", ctypes.c_void_p)]
+
+
+_bound = None
+
+
+def lib() -> ctypes.CDLL:
+    global _bound
+    if _bound is None:
+        L = _lib.lib()
+        P, I, Z, F, L64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float, ctypes.c_int64
+        route = [P, L64, I, I, I, I, I, F]      # logits, ld, dtype, tokens, n_expert, topk, flags, scale
+        L.moe_route.argtypes = route + [P, P, P]
+        L.moe_balance_bytes.argtypes = [I, I, I]
+        L.moe_balance_bytes.restype = Z
+        L.moe_route_balance.argtypes = route + [P, I, F, P, P, P, P, P, P, Z, P]
+        L.moe_route_backward.argtypes = route + [P, P, P, I, F, P, P, P, L64, P]
+        L.moe_combine_backward.argtypes = [P, P, P, I, I, I, P, P, P]
+        L.moe_adapters_bytes.argtypes = [ctypes.POINTER(moe_adapter_set), I]
+        L.moe_adapters_bytes.restype = Z
+        L.moe_adapters.argtypes = [ctypes.POINTER(moe_adapter_set), P, I, I, P, L64, P, L64, P, L64, P, Z, P]
+        for name in EXPORTS:
+            if not name.endswith("_bytes"):
+                getattr(L, name).restype = I
+        _bound = L
+    return _bound
+
+
+def _dtype(t, what: str) -> int:
+    import torch
+    code = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}.get(t.dtype)
+    if code is None:
+        raise MoeError(-3, f"{what}: {t.dtype}")
+    return code
+
+
+def _arg(t, what: str, dtype, shape):
+    """A dense tensor of the given type and shape on the current device -> its address."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise MoeError(-3, f"{what}: {t.dtype} instead of {dtype}")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise MoeError(-1, f"{what}: shape {tuple(t.shape)}, strides {t.stride()}; dense {tuple(shape)} wanted")
+    return _address(t, what)
+
+
+def _rows(t, what: str, shape):
+    """A matrix with dense rows -> its address and row stride in elements."""
+    if tuple(t.shape) != tuple(shape) or (t.dim() == 2 and t.shape[1] > 1 and t.stride(1) != 1):
+        raise MoeError(-1, f"{what}: shape {tuple(t.shape)}, strides {t.stride()}; {tuple(shape)} with dense rows wanted")
+    # the stride of a single row says nothing: torch may give it any value
+    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return _address(t, what), ld
+
+
+def _address(t, what: str):
+    import torch
+    if not t.is_cuda:
+        raise MoeError(-1, f"{what}: on {t.device}, not in device memory")
+    if t.device.index != torch.cuda.current_device():
+        raise MoeError(-1, f"{what}: on {t.device}, the current device is {torch.cuda.current_device()}")
+    return t.data_ptr()
+
+
+def _out_of_place(t, what: str):
+    """Rows that are written: no two of them may overlap."""
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise MoeError(-1, f"{what}: rows overlap (strides {t.stride()})")
+
+
+def _route(logits, topk: int, renorm: bool, scale: float):
+    if logits.dim() != 2:
+        raise MoeError(-1, f"logits: shape {tuple(logits.shape)}")
+    ptr, ld = _rows(logits, "logits", logits.shape)
+    T, E = logits.shape
+    return (ptr, ld, _dtype(logits, "logits"), T, E, topk, MOE_ROUTE_RENORM if renorm else 0, scale)
+
+
+def _matrix(t, what: str):
+    if t.dim() != 2:
+        raise MoeError(-1, f"{what}: shape {tuple(t.shape)}")
+    return t.shape
+
+
+def moe_route(logits, ids, w, renorm: bool = True, scale: float = 1.0, stream=None):
+    """logits [T, E] (fp32, bf16 or fp16, dense rows) -> ids int32 [T, topk], w fp32 [T, topk]."""
+    import torch
+    T, K = _matrix(ids, "ids")
+    head = _route(logits, K, renorm, scale)
+    _lib._check(lib().moe_route(*head, _arg(ids, "ids", torch.int32, (head[3], K)),
+                                _arg(w, "w", torch.float32, (head[3], K)), _lib._stream(stream)), "moe_route")
+
+
+def moe_balance_bytes(tokens: int, n_expert: int, n_seq: int) -> int:
+    return int(lib().moe_balance_bytes(tokens, n_expert, n_seq))
+
+
+def moe_route_balance(logits, seq_off, coef: float, ids, w, counts, probs, loss, workspace,
+                      renorm: bool = True, scale: float = 1.0, stream=None):
+    """moe_route with the balance statistics of the sequences seq_off (int32 [S+1]) bounds:
+    counts int32 [S, E], probs fp32 [S, E], loss fp32 [1]."""
+    import torch
+    T, K = _matrix(ids, "ids")
+    head = _route(logits, K, renorm, scale)
+    T, E, S = head[3], head[4], seq_off.numel() - 1
+    f32, i32 = torch.float32, torch.int32
+    _lib._check(lib().moe_route_balance(
+        *head, _arg(seq_off, "seq_off", i32, (S + 1,)), S, coef, _arg(ids, "ids", i32, (T, K)),
+        _arg(w, "w", f32, (T, K)), _arg(counts, "counts", i32, (S, E)), _arg(probs, "probs", f32, (S, E)),
+        _arg(loss, "loss", f32, (1,)), _address(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), _lib._stream(stream)), "moe_route_balance")
+
+
+def moe_route_backward(logits, ids, dw, dlogits, renorm: bool = True, scale: float = 1.0, seq_off=None,
+                       coef: float = 0.0, counts=None, dloss=None, stream=None):
+    """The gradient of moe_route / moe_route_balance: dw fp32 [T, topk] (or None) and the loss's
+    (seq_off and counts of the forward call, dloss fp32 [1] or None for 1) -> dlogits, the
+    logits' type and shape."""
+    import torch
+    T, K = _matrix(ids, "ids")
+    head = _route(logits, K, renorm, scale)
+    T, E = head[3], head[4]
+    S = 0 if seq_off is None else seq_off.numel() - 1
+    f32, i32 = torch.float32, torch.int32
+    if dlogits.dtype != logits.dtype:
+        raise MoeError(-3, f"dlogits: {dlogits.dtype} instead of {logits.dtype}")
+    d_ptr, ldd = _rows(dlogits, "dlogits", (T, E))
+    _out_of_place(dlogits, "dlogits")
+    _lib._check(lib().moe_route_backward(
+        *head, _arg(ids, "ids", i32, (T, K)), _arg(dw, "dw", f32, (T, K)),
+        _arg(seq_off, "seq_off", i32, (S + 1,)), S, coef, _arg(counts, "counts", i32, (S, E)),
+        _arg(dloss, "dloss", f32, (1,)), d_ptr, ldd, _lib._stream(stream)), "moe_route_backward")
+
+
+def moe_combine_backward(dm, w, dout, dw, ddm=None, stream=None):
+    """The gradient of moe_combine: dout fp32 [T, H] -> dw fp32 [T, topk] and ddm fp32
+    [T*topk, H] (either may be None; dm is read for dw, w [T, topk] for ddm)."""
+    import torch
+    f32 = torch.float32
+    T, H = _matrix(dout, "dout")
+    of = dw if dw is not None else w
+    if of is None:
+        raise MoeError(-1, "moe_combine_backward: neither dw nor w")
+    K = _matrix(of, "dw" if dw is not None else "w")[1]
+    _lib._check(lib().moe_combine_backward(
+        _arg(dm, "dm", f32, (T * K, H)), _arg(w, "w", f32, (T, K)), _arg(dout, "dout", f32, (T, H)),
+        T, K, H, _arg(dw, "dw", f32, (T, K)), _arg(ddm, "ddm", f32, (T * K, H)), _lib._stream(stream)),
+        "moe_combine_backward")
+
+
+class AdapterSet:
+    """The adapters of one projection (kept alive here, read in place): a
+    [n, rank, n_in] and b [n, n_out, rank], both bf16 or both fp16, scale fp32
+    [n], rank int32 [n] with each adapter's own rank (None: all full)."""
+
+    def __init__(self, a, b, scale, rank=None):
+        import torch
+        if a.dim() != 3 or b.dim() != 3:
+            raise MoeError(-1, f"AdapterSet: a {tuple(a.shape)}, b {tuple(b.shape)}")
+        n, r, n_in = a.shape
+        n_out = b.shape[1]
+        code = _dtype(a, "a")
+        if code == MOE_F32:
+            raise MoeError(-3, f"a: {a.dtype}")
+        self.tensors = (a, b, scale, rank)
+        self.n_in, self.n_out, self.rank = n_in, n_out, r
+        self.struct = moe_adapter_set(
+            code, n, r, n_in, n_out, _arg(a, "a", a.dtype, (n, r, n_in)), _arg(b, "b", a.dtype, (n, n_out, r)),
+            _arg(scale, "scale", torch.float32, (n,)), _arg(rank, "rank", torch.int32, (n,)))
+
+
+def moe_adapters_bytes(adapters: AdapterSet, tokens: int) -> int:
+    return int(lib().moe_adapters_bytes(ctypes.byref(adapters.struct), tokens))
+
+
+def moe_adapters(adapters: AdapterSet, ids, x, base, out, workspace, stream=None):
+    """out = base + each row's adapter over x: ids int32 [T] (negative: none), x [T, n_in], base
+    and out [T, n_out] of fp32 or the set's type, dense rows; out may be base."""
+    import torch
+    T = ids.numel()
+    x_ptr, ldx = _rows(x, "x", (T, adapters.n_in))
+    b_ptr, ldb = _rows(base, "base", (T, adapters.n_out))
+    o_ptr, ldo = _rows(out, "out", (T, adapters.n_out))
+    _out_of_place(out, "out")
+    if not (x.dtype == base.dtype == out.dtype):
+        raise MoeError(-3, f"moe_adapters: x {x.dtype}, base {base.dtype}, out {out.dtype}")
+    _lib._check(lib().moe_adapters(
+        ctypes.byref(adapters.struct), _arg(ids, "ids", torch.int32, (T,)), T, _dtype(x, "x"), x_ptr, ldx,
+        b_ptr, ldb, o_ptr, ldo, _address(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), _lib._stream(stream)), "moe_adapters")

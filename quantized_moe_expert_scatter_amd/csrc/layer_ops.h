@@ -1,0 +1,100 @@
+// layer_ops.h -- launchers of the steps around the expert products
+// (moe_layer.cpp checks the arguments, the .hip files hold the kernels).
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+
+#include <cstddef>
+#include <cstdint>
+
+namespace moe {
+
+// The router's rows: logits and what the router makes of them.
+struct RouteArgs {
+    const void *logits;
+    int64_t ld;
+    int dtype;                 // moe_dtype
+    int tokens, n_expert, topk;
+    bool renorm;
+    float scale;
+    int32_t *ids;              // forward: out; backward: in
+    float *w;                  // forward: out
+    // balance statistics
+    const int32_t *seq_off;    // NULL: none
+    int n_seq;
+    float coef;
+    int32_t *counts;           // forward: out; backward: in
+    float *probs;
+    float *loss;
+    uint8_t *ws;
+    // gradient
+    const float *dw;
+    const float *dloss;
+    void *dlogits;
+    int64_t ldd;
+};
+
+// The balance statistics are summed in pieces: the tokens are cut into ranges
+// of range_tokens, one workgroup each, and a range's part of a sequence is a
+// piece.  Sequences are in token order, so (range, sequence) -> range +
+// sequence numbers the pieces without collisions, and no kernel needs to know
+// on the host where sequences begin.
+struct BalanceLayout {
+    int range_tokens, n_ranges;
+    size_t probs;      // fp32 [n_ranges + n_seq][E]: sums of p over a piece
+    size_t counts;     // int32, the same shape
+    size_t loss;       // fp32 [n_seq][column blocks]: parts of the loss
+    size_t total;
+};
+
+constexpr int kBalanceCols = 64;         // columns of one joining workgroup
+constexpr int kBalanceMaxRanges = 1024;  // four workgroups per CU
+constexpr int kBalanceMinRange = 4;      // one token per wave
+
+inline BalanceLayout balance_layout(int tokens, int n_expert, int n_seq) {
+    BalanceLayout L{};
+    const int per = int(((long long)tokens + kBalanceMaxRanges - 1) / kBalanceMaxRanges);
+    L.range_tokens = per > kBalanceMinRange ? (per + 3) / 4 * 4 : kBalanceMinRange;
+    L.n_ranges = int(((long long)tokens + L.range_tokens - 1) / L.range_tokens);
+    const size_t cells = (size_t(L.n_ranges) + size_t(n_seq)) * size_t(n_expert);
+    auto up = [](size_t x) { return (x + 15) & ~size_t(15); };
+    size_t o = 0;
+    L.probs = o;  o += up(cells * 4);
+    L.counts = o; o += up(cells * 4);
+    L.loss = o;   o += up(size_t(n_seq) * size_t((n_expert + kBalanceCols - 1) / kBalanceCols) * 4);
+    L.total = o;
+    return L;
+}
+
+hipError_t launch_route(const RouteArgs &a, hipStream_t stream);
+hipError_t launch_route_balance(const RouteArgs &a, hipStream_t stream);
+hipError_t launch_route_backward(const RouteArgs &a, hipStream_t stream);
+
+// dw[t][k] = dout[t] . dm[t*topk+k], ddm[t*topk+k] = w[t][k] * dout[t] (either may be NULL)
+hipError_t launch_combine_backward(const float *dm, const float *w, const float *dout, int tokens,
+                                   int topk, int hidden, float *dw, float *ddm, hipStream_t stream);
+
+struct AdapterArgs {
+    int wtype, dtype;          // moe_dtype of the matrices and of x, base, out
+    int n_adapter, rank, n_in, n_out;
+    const void *a, *b;
+    const float *scale;
+    const int32_t *ranks;
+    const int32_t *ids;
+    int tokens;
+    const void *x;
+    int64_t ldx;
+    const void *base;
+    int64_t ldb;
+    void *out;
+    int64_t ldo;
+    float *ws;
+};
+// The rows' low-rank values, fp32 [tokens][rank].
+inline size_t adapter_workspace(int tokens, int rank, int n_in) {
+    (void)n_in;
+    return (size_t(tokens) * size_t(rank) * 4 + 15) & ~size_t(15);
+}
+hipError_t launch_adapters(const AdapterArgs &a, hipStream_t stream);
+
+}  // namespace moe

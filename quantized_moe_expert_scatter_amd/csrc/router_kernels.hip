@@ -1,0 +1,432 @@
+// router_kernels.hip -- the router's choice, its balance statistics and its
+// gradient.
+//
+// One wavefront takes one token: lane i holds the J logits of experts
+// [i*J, (i+1)*J), J = n_expert / 64 rounded up to a power of two, so a row is
+// read once, in wide loads, and every later step is in registers.
+//
+// The choice: logits become 32-bit keys of the same order, and topk times the
+// wave takes its largest key.  Lanes hold ascending experts, so the first
+// lane that has the key, and in it the first, is the lowest expert.
+#include "layer_ops.h"
+#include "wave.cuh"
+
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+namespace moe {
+
+namespace {
+
+constexpr int kRouteThreads = 256;
+constexpr int kRouteWaves = kRouteThreads / 64;
+constexpr int kRouteMaxGroups = 16384;      // workgroups; further tokens in a loop
+constexpr int kJoinWaves = 16;
+constexpr int kJoinMaxGroups = 4096;        // workgroups of the joining kernel; further jobs in a loop
+
+// float -> key: ascending like the number, -0 equal to +0, NaN above +inf.
+// No logit's key is 0 (that of -inf is 0x007fffff): 0 marks a place that
+// holds no expert, or one already taken.
+__device__ __forceinline__ uint32_t order_key(float f) {
+    if (f != f) return 0xffffffffu;
+    const uint32_t u = __float_as_uint(f + 0.0f);
+    return (u >> 31) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return __uint_as_float((k >> 31) ? (k & 0x7fffffffu) | ((k == 0xffffffffu) ? 0x7fffffffu : 0u) : ~k);
+}
+
+template <int J, int DT, bool VEC>
+__device__ __forceinline__ void load_row(const void *logits, int64_t at, int n_expert, int lane,
+                                         float (&v)[J]) {
+    using T = typename Elem<DT>::T;
+    const T *row = static_cast<const T *>(logits) + at + lane * J;
+    if constexpr (VEC) {
+        struct alignas(J * sizeof(T) < 16 ? J * sizeof(T) : 16) Run { T e[J]; };
+        Run r;
+        if (lane * J < n_expert) r = *reinterpret_cast<const Run *>(row);
+#pragma unroll
+        for (int j = 0; j < J; ++j) v[j] = lane * J < n_expert ? to_float<DT>(r.e[j]) : -INFINITY;
+    } else {
+#pragma unroll
+        for (int j = 0; j < J; ++j) v[j] = lane * J + j < n_expert ? to_float<DT>(row[j]) : -INFINITY;
+    }
+}
+
+// The topk largest: lane k < topk receives the k-th's expert and logit.
+// Returns the row's largest logit (NaN if the row holds one).
+template <int J>
+__device__ __forceinline__ float choose(const float (&v)[J], int n_expert, int topk, int lane, int &id,
+                                        float &logit) {
+    uint32_t key[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) key[j] = lane * J + j < n_expert ? order_key(v[j]) : 0u;
+    uint32_t first = 0, mine = 0;
+    id = 0;
+    for (int k = 0; k < topk; ++k) {
+        uint32_t best = key[0];
+#pragma unroll
+        for (int j = 1; j < J; ++j) best = max(best, key[j]);
+        const uint32_t top = wave_max(best);
+        const int owner = __ffsll((unsigned long long)__ballot(best == top)) - 1;
+        int at = 0;
+#pragma unroll
+        for (int j = J - 1; j >= 0; --j) at = key[j] == top ? j : at;
+        const int expert = owner * J + __builtin_amdgcn_readlane(at, owner);
+#pragma unroll
+        for (int j = 0; j < J; ++j) key[j] = (lane * J + j == expert) ? 0u : key[j];
+        if (lane == k) {
+            id = expert;
+            mine = top;
+        }
+        if (k == 0) first = top;
+    }
+    logit = key_value(mine);
+    return key_value(first);
+}
+
+// What the exponents are taken against: the row's largest logit, 0 where every
+// expert is closed (all exponentials are then 0).
+__device__ __forceinline__ float softmax_shift(float top) { return top == -INFINITY ? 0.0f : top; }
+
+// First sequence with seq_off[s+1] > t (n_seq if none), by 64 probes a step.
+__device__ __forceinline__ int sequence_of(const int32_t *seq_off, int n_seq, int t, int lane) {
+    int lo = 0, n = n_seq;              // the answer is in [lo, lo + n]
+    while (n > 0) {
+        const int step = (n + 63) / 64;
+        const int i = lo + (lane + 1) * step - 1;
+        const bool past = lane * step < n && seq_off[1 + min(i, lo + n - 1)] <= t;
+        const int skip = __popcll(__ballot(past)) * step;
+        if (skip >= n) return lo + n;
+        lo += skip;
+        n = min(step - 1, n - skip);
+    }
+    return lo;
+}
+
+// Routes token t; with STATS the row's softmax is added to acc.
+template <int J, int DT, bool VEC, bool STATS>
+__device__ __forceinline__ void route_token(const RouteArgs &a, int t, int lane, bool count,
+                                            float (&acc)[J], int *hist) {
+    float v[J];
+    load_row<J, DT, VEC>(a.logits, int64_t(t) * a.ld, a.n_expert, lane, v);
+    int id;
+    float logit;
+    const float top = choose<J>(v, a.n_expert, a.topk, lane, id, logit);
+    const float shift = softmax_shift(top);
+    const bool chosen = lane < a.topk;
+    const float e = chosen ? expf(logit - shift) : 0.0f;
+    float inv = 0.0f;
+    if (STATS || !a.renorm) {
+        float part = 0.0f;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            v[j] = expf(v[j] - shift);
+            part += v[j];
+        }
+        const float sum = wave_sum(part);
+        inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        if (STATS && count) {
+#pragma unroll
+            for (int j = 0; j < J; ++j) acc[j] = __builtin_fmaf(v[j], inv, acc[j]);
+        }
+    }
+    if (a.renorm) {
+        const float sum = wave_sum(e);
+        inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    }
+    if (chosen) {
+        a.ids[int64_t(t) * a.topk + lane] = id;
+        a.w[int64_t(t) * a.topk + lane] = a.scale * (e * inv);
+        if (STATS && count && logit != -INFINITY) atomicAdd(hist + id, 1);
+    }
+}
+
+template <int J, int DT, bool VEC>
+__global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
+    const int lane = threadIdx.x & 63;
+    float none[J];
+    for (int64_t t = int64_t(blockIdx.x) * kRouteWaves + (threadIdx.x >> 6); t < a.tokens;
+         t += int64_t(gridDim.x) * kRouteWaves)
+        route_token<J, DT, VEC, false>(a, int(t), lane, false, none, nullptr);
+}
+
+// One workgroup per range of tokens: routes them and sums each sequence's part
+// of the range, p in registers (then over the four waves through LDS), the
+// choices in an LDS histogram.
+template <int J, int DT, bool VEC>
+__global__ __launch_bounds__(kRouteThreads) void route_balance_kernel(RouteArgs a, BalanceLayout L) {
+    __shared__ float red[kRouteWaves][64 * J];
+    __shared__ int hist[64 * J];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    float *out_p = reinterpret_cast<float *>(a.ws + L.probs);
+    int32_t *out_c = reinterpret_cast<int32_t *>(a.ws + L.counts);
+    const int t0 = int(blockIdx.x) * L.range_tokens;
+    const int t1 = a.tokens - t0 < L.range_tokens ? a.tokens : t0 + L.range_tokens;
+    for (int e = threadIdx.x; e < 64 * J; e += kRouteThreads) hist[e] = 0;
+    __syncthreads();
+    float acc[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) acc[j] = 0.0f;
+    for (int pos = t0; pos < t1;) {
+        const int s = sequence_of(a.seq_off, a.n_seq, pos, lane);
+        int end = t1;
+        bool inside = s < a.n_seq;
+        if (inside) {
+            const int b = a.seq_off[s], e = a.seq_off[s + 1];
+            if (pos < b) {              // in front of the first sequence
+                inside = false;
+                end = min(b, t1);
+            } else if (e > pos) {
+                end = min(e, t1);
+            }
+        }
+        for (int t = pos + wave; t < end; t += kRouteWaves)
+            route_token<J, DT, VEC, true>(a, t, lane, inside, acc, hist);
+        if (inside) {
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                red[wave][lane * J + j] = acc[j];
+                acc[j] = 0.0f;
+            }
+            __syncthreads();
+            const size_t at = (size_t(blockIdx.x) + s) * a.n_expert;
+            for (int e = threadIdx.x; e < a.n_expert; e += kRouteThreads) {
+                out_p[at + e] = (red[0][e] + red[1][e]) + (red[2][e] + red[3][e]);
+                out_c[at + e] = hist[e];
+                hist[e] = 0;
+            }
+            __syncthreads();
+        }
+        pos = end;
+    }
+}
+
+// Joins a sequence's pieces for 64 experts: a wave takes every 16th piece, the
+// waves are added in order.  Long sums in 64 bits.
+__global__ __launch_bounds__(64 * kJoinWaves) void balance_join_kernel(RouteArgs a, BalanceLayout L,
+                                                                       int cols) {
+    __shared__ double red_p[kJoinWaves][kBalanceCols];
+    __shared__ int red_c[kJoinWaves][kBalanceCols];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t jobs = int64_t(a.n_seq) * cols;
+    for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
+        const int s = int(job / cols), e = int(job % cols) * kBalanceCols + lane;
+        const int b = min(max(a.seq_off[s], 0), a.tokens);
+        const int n = min(max(a.seq_off[s + 1], b), a.tokens) - b;
+        double p = 0.0;
+        int c = 0;
+        if (n > 0 && e < a.n_expert) {
+            const float *in_p = reinterpret_cast<const float *>(a.ws + L.probs);
+            const int32_t *in_c = reinterpret_cast<const int32_t *>(a.ws + L.counts);
+            const int last = (b + n - 1) / L.range_tokens;
+            for (int r = b / L.range_tokens + wave; r <= last; r += kJoinWaves) {
+                const size_t at = (size_t(r) + s) * a.n_expert + e;
+                p += double(in_p[at]);
+                c += in_c[at];
+            }
+        }
+        red_p[wave][lane] = p;
+        red_c[wave][lane] = c;
+        __syncthreads();
+        if (wave == 0) {
+            for (int i = 1; i < kJoinWaves; ++i) {
+                p += red_p[i][lane];
+                c += red_c[i][lane];
+            }
+            const float mean = n > 0 ? float(p / n) : 0.0f;
+            if (e < a.n_expert) {
+                a.counts[size_t(s) * a.n_expert + e] = c;
+                a.probs[size_t(s) * a.n_expert + e] = mean;
+            }
+            const float part = wave_sum(float(c) * mean);
+            if (lane == 0)
+                reinterpret_cast<float *>(a.ws + L.loss)[job] =
+                    n > 0 ? part * (float(a.n_expert) / (float(a.topk) * float(n))) : 0.0f;
+        }
+        __syncthreads();
+    }
+}
+
+__global__ __launch_bounds__(1024) void balance_loss_kernel(RouteArgs a, BalanceLayout L, int64_t parts) {
+    __shared__ double red[1024];
+    const float *in = reinterpret_cast<const float *>(a.ws + L.loss);
+    double sum = 0.0;
+    for (int64_t i = threadIdx.x; i < parts; i += 1024) sum += double(in[i]);
+    red[threadIdx.x] = sum;
+    __syncthreads();
+    for (int half = 512; half > 0; half >>= 1) {
+        if (int(threadIdx.x) < half) red[threadIdx.x] += red[threadIdx.x + half];
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) a.loss[0] = float(double(a.coef) / a.n_seq * red[0]);
+}
+
+// The gradient of one token's row.
+template <int J, int DT, bool VEC>
+__global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteArgs a) {
+    using T = typename Elem<DT>::T;
+    const int lane = threadIdx.x & 63;
+    const float dloss = a.seq_off && a.dloss ? a.dloss[0] : 1.0f;
+    for (int64_t t = int64_t(blockIdx.x) * kRouteWaves + (threadIdx.x >> 6); t < a.tokens;
+         t += int64_t(gridDim.x) * kRouteWaves) {
+        float v[J];
+        load_row<J, DT, VEC>(a.logits, t * a.ld, a.n_expert, lane, v);
+        // the chosen experts: lane k has the k-th
+        int id = -1;
+        float g = 0.0f, logit = -INFINITY;
+        if (lane < a.topk) {
+            id = a.ids[t * a.topk + lane];
+            if (id < 0 || id >= a.n_expert) id = -1;
+            if (id >= 0) {
+                logit = to_float<DT>(static_cast<const T *>(a.logits)[t * a.ld + id]);
+                if (a.dw) g = a.scale * a.dw[t * a.topk + lane];
+            }
+        }
+        // the loss's part
+        float c[J];
+#pragma unroll
+        for (int j = 0; j < J; ++j) c[j] = 0.0f;
+        if (a.seq_off) {
+            const int s = sequence_of(a.seq_off, a.n_seq, int(t), lane);
+            if (s < a.n_seq && t >= a.seq_off[s]) {
+                const float n = float(a.seq_off[s + 1] - a.seq_off[s]);
+                const float f = dloss * a.coef * float(a.n_expert) /
+                                (float(a.n_seq) * float(a.topk) * n * n);
+                const int32_t *counts = a.counts + size_t(s) * a.n_expert + lane * J;
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+                    if (lane * J + j < a.n_expert) c[j] = f * float(counts[j]);
+            }
+        }
+        uint32_t best = 0;
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            best = max(best, lane * J + j < a.n_expert ? order_key(v[j]) : 0u);
+        const float shift = softmax_shift(key_value(wave_max(best)));
+        float part = 0.0f, pc = 0.0f;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            v[j] = expf(v[j] - shift);
+            part += v[j];
+            pc = __builtin_fmaf(v[j], c[j], pc);
+        }
+        const float sum = wave_sum(part);
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        float z = wave_sum(pc) * inv;
+        float e = id >= 0 ? expf(logit - shift) : 0.0f;
+        float add;
+        if (a.renorm) {
+            const float chosen = wave_sum(e);
+            const float q = chosen == 0.0f ? 0.0f : e / chosen;
+            add = q * (g - wave_sum(q * g));
+        } else {
+            add = e * inv * g;
+            z += wave_sum(add);
+        }
+#pragma unroll
+        for (int j = 0; j < J; ++j) v[j] = v[j] * inv * (c[j] - z);
+        for (int k = 0; k < a.topk; ++k) {
+            const int expert = __builtin_amdgcn_readlane(id, k);
+            const float x = __uint_as_float(uint32_t(__builtin_amdgcn_readlane(int(__float_as_uint(add)), k)));
+#pragma unroll
+            for (int j = 0; j < J; ++j) v[j] += lane * J + j == expert ? x : 0.0f;
+        }
+        T *row = static_cast<T *>(a.dlogits) + t * a.ldd + lane * J;
+        if constexpr (VEC) {
+            struct alignas(J * sizeof(T) < 16 ? J * sizeof(T) : 16) Run { T e[J]; };
+            Run r;
+#pragma unroll
+            for (int j = 0; j < J; ++j) r.e[j] = from_float<DT>(v[j]);
+            if (lane * J < a.n_expert) *reinterpret_cast<Run *>(row) = r;
+        } else {
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                if (lane * J + j < a.n_expert) row[j] = from_float<DT>(v[j]);
+        }
+    }
+}
+
+// Lanes hold J experts each; wide loads need whole runs of J at a multiple of
+// their size, at every row.
+int experts_per_lane(int n_expert) {
+    int j = 1;
+    while (j * 64 < n_expert) j *= 2;
+    return j;
+}
+bool wide_rows(int j, int n_expert, int64_t ld, int dtype) {
+    const int size = dtype == kF32 ? 4 : 2;
+    const int run = j * size < 16 ? j * size : 16;
+    return n_expert % j == 0 && ld * size % run == 0;
+}
+
+// Calls f(J, DT, VEC) as compile-time constants.
+template <class F>
+hipError_t by_shape(int j, int dtype, bool vec, F f) {
+    auto with_dt = [&](auto J) {
+        auto with_vec = [&](auto DT) {
+            return vec ? f(J, DT, std::true_type{}) : f(J, DT, std::false_type{});
+        };
+        if (dtype == kF32) return with_vec(std::integral_constant<int, kF32>{});
+        if (dtype == kBF16) return with_vec(std::integral_constant<int, kBF16>{});
+        return with_vec(std::integral_constant<int, kF16>{});
+    };
+    switch (j) {
+        case 1: return with_dt(std::integral_constant<int, 1>{});
+        case 2: return with_dt(std::integral_constant<int, 2>{});
+        case 4: return with_dt(std::integral_constant<int, 4>{});
+        case 8: return with_dt(std::integral_constant<int, 8>{});
+        case 16: return with_dt(std::integral_constant<int, 16>{});
+        default: return with_dt(std::integral_constant<int, 32>{});
+    }
+}
+
+dim3 token_grid(int tokens) {
+    const int64_t groups = (int64_t(tokens) + kRouteWaves - 1) / kRouteWaves;
+    return dim3(unsigned(groups < kRouteMaxGroups ? groups : kRouteMaxGroups));
+}
+
+}  // namespace
+
+hipError_t launch_route(const RouteArgs &a, hipStream_t stream) {
+    const int j = experts_per_lane(a.n_expert);
+    return by_shape(j, a.dtype, wide_rows(j, a.n_expert, a.ld, a.dtype), [&](auto J, auto DT, auto V) {
+        hipLaunchKernelGGL((route_kernel<J.value, DT.value, V.value>), token_grid(a.tokens),
+                           dim3(kRouteThreads), 0, stream, a);
+        return hipGetLastError();
+    });
+}
+
+hipError_t launch_route_balance(const RouteArgs &a, hipStream_t stream) {
+    const BalanceLayout L = balance_layout(a.tokens, a.n_expert, a.n_seq);
+    const int j = experts_per_lane(a.n_expert);
+    hipError_t err = hipSuccess;
+    if (a.tokens > 0)
+        err = by_shape(j, a.dtype, wide_rows(j, a.n_expert, a.ld, a.dtype), [&](auto J, auto DT, auto V) {
+            hipLaunchKernelGGL((route_balance_kernel<J.value, DT.value, V.value>), dim3(L.n_ranges),
+                               dim3(kRouteThreads), 0, stream, a, L);
+            return hipGetLastError();
+        });
+    if (err != hipSuccess) return err;
+    const int cols = (a.n_expert + kBalanceCols - 1) / kBalanceCols;
+    const int64_t jobs = int64_t(cols) * a.n_seq;
+    hipLaunchKernelGGL(balance_join_kernel, dim3(unsigned(jobs < kJoinMaxGroups ? jobs : kJoinMaxGroups)),
+                       dim3(64 * kJoinWaves), 0, stream, a, L, cols);
+    err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    hipLaunchKernelGGL(balance_loss_kernel, dim3(1), dim3(1024), 0, stream, a, L, jobs);
+    return hipGetLastError();
+}
+
+hipError_t launch_route_backward(const RouteArgs &a, hipStream_t stream) {
+    const int j = experts_per_lane(a.n_expert);
+    const bool vec = wide_rows(j, a.n_expert, a.ld, a.dtype) && wide_rows(j, a.n_expert, a.ldd, a.dtype);
+    return by_shape(j, a.dtype, vec, [&](auto J, auto DT, auto V) {
+        hipLaunchKernelGGL((route_backward_kernel<J.value, DT.value, V.value>), token_grid(a.tokens),
+                           dim3(kRouteThreads), 0, stream, a);
+        return hipGetLastError();
+    });
+}
+
+}  // namespace moe

@@ -1,4 +1,5 @@
-"""One MoE layer's routed-expert product on the device: buffers + the four steps.
+"""One MoE layer's routed-expert product on the device: buffers + the four steps,
+and, for a layer routed on the device, the steps around them.
 
 Plumbing only: torch provides device memory and the stream, the C ABI does
 every step of the computation.
@@ -7,7 +8,7 @@ from __future__ import annotations
 
 import numpy as np
 
-from . import _lib
+from . import _lib, _steps
 from .workloads import ExpertWeights
 
 
@@ -21,6 +22,13 @@ class DeviceLayer:
 
     x: float32 [T, hidden]; ids: int32 [T, topk]; w_gu / w_down: ExpertWeights
     (row-major planes; packed here into the kernels' tiled layout).
+    logits (float32 [T, n_expert], instead of ids and route_w): the layer is
+    routed on the device, topk experts a token, and planned there (route());
+    seq_off (int32 [S+1]) and balance_coef add the balance statistics and loss
+    of those sequences.  adapters (an AdapterSet of [hidden -> hidden]) and
+    adapter_ids (int32 [T]) add each row's adapter to the layer's output.
+    forward() runs all of it, backward() takes the output's gradient to the
+    logits (the experts are frozen).
     Buffers: xq (q8_1 rows of hidden), gu (fp32 [R, 2*n_ff]), hq (q8_1 rows of
     n_ff), dm (fp32 [T*topk, hidden]); R = T*topk.
     guard > 0 (tests): every output buffer sits between two guard regions of
@@ -32,13 +40,16 @@ class DeviceLayer:
 
     def __init__(self, x: np.ndarray, ids: np.ndarray, w_gu: ExpertWeights, w_down: ExpertWeights,
                  chunk_rows: int = 128, device="cuda", stream=None, route_w: np.ndarray = None,
-                 device_plan: bool = False, gu_interleaved: bool = False, guard: int = 0):
+                 device_plan: bool = False, gu_interleaved: bool = False, guard: int = 0,
+                 logits: np.ndarray = None, topk: int = None, renorm: bool = True,
+                 seq_off: np.ndarray = None, balance_coef: float = 0.0, adapters=None,
+                 adapter_ids: np.ndarray = None):
         import torch
         self.device = torch.device(device)
         self.guard = (guard + 255) // 256 * 256
         self._guarded = {}
         self.tokens, self.hidden = x.shape
-        self.topk = ids.shape[1]
+        self.topk = ids.shape[1] if logits is None else topk
         self.n_expert = w_gu.n_expert
         self.n_ff = w_gu.rows // 2
         self.rows = self.tokens * self.topk
@@ -60,7 +71,15 @@ class DeviceLayer:
         self.route_w = _to_device(rw.astype(np.float32, copy=False).reshape(-1)
                                   if rw.size else np.zeros(4, np.float32), self.device)
         self.out = self._buffer("out", (max(self.tokens, 1), self.hidden), f32)
-        if device_plan:
+        self.adapters, self.adapter_ids = adapters, None
+        if adapters is not None:
+            self.adapter_ids = _to_device(np.ascontiguousarray(adapter_ids, np.int32), self.device)
+            n = _steps.moe_adapters_bytes(adapters, self.tokens)
+            self.adapter_ws = self._buffer("adapter_ws", (max(n, 16),), u8)
+        self.logits = None
+        if logits is not None:
+            self._routed(logits, renorm, seq_off, balance_coef, stream)
+        elif device_plan:
             # the routing ids go up first and the plan is built from them on the GPU
             self.ids_dev = _to_device(np.ascontiguousarray(ids, np.int32).reshape(-1)
                                       if ids.size else np.zeros(4, np.int32), self.device)
@@ -70,6 +89,65 @@ class DeviceLayer:
         else:
             self.plan = _lib.moe_prefill_plan(ids, self.n_expert, chunk_rows, self.w_gu, self.w_dn,
                                               workspace=self.workspace, stream=stream)
+
+    def _routed(self, logits, renorm, seq_off, coef, stream):
+        import torch
+        i32, f32 = torch.int32, torch.float32
+        T, E = self.tokens, self.n_expert
+        self.logits = _to_device(logits.astype(np.float32, copy=False), self.device)
+        self.renorm, self.balance_coef = renorm, coef
+        self.ids_dev = self._buffer("ids", (T, self.topk), i32)
+        self.route_w = self._buffer("route_w", (T, self.topk), f32)
+        self.dw = self._buffer("dw", (T, self.topk), f32)
+        self.dlogits = self._buffer("dlogits", (T, E), f32)
+        self.seq_off = None
+        if seq_off is not None:
+            self.seq_off = _to_device(np.ascontiguousarray(seq_off, np.int32), self.device)
+            S = self.seq_off.numel() - 1
+            self.counts = self._buffer("counts", (S, E), i32)
+            self.probs = self._buffer("probs", (S, E), f32)
+            self.loss = self._buffer("loss", (1,), f32)
+            self.balance_ws = self._buffer("balance_ws", (_steps.moe_balance_bytes(T, E, S),), torch.uint8)
+        self.plan = None
+        self.route(stream)
+
+    def route(self, stream=None):
+        """Routes the logits and plans the layer for the choice, on the device."""
+        if self.seq_off is None:
+            _steps.moe_route(self.logits, self.ids_dev, self.route_w, renorm=self.renorm, stream=stream)
+        else:
+            _steps.moe_route_balance(self.logits, self.seq_off, self.balance_coef, self.ids_dev, self.route_w,
+                                     self.counts, self.probs, self.loss, self.balance_ws, renorm=self.renorm,
+                                     stream=stream)
+        if self.plan is not None:
+            self.plan.close()
+        self.plan = _lib.moe_prefill_plan_device(self.ids_dev, self.tokens, self.topk, self.n_expert,
+                                                 self.chunk_rows, self.w_gu, self.w_dn, self.workspace, stream)
+
+    def apply_adapters(self, stream=None):
+        """Adds each row's adapter to the layer's output, in place."""
+        _steps.moe_adapters(self.adapters, self.adapter_ids, self.x, self.out[:self.tokens],
+                            self.out[:self.tokens], self.adapter_ws, stream)
+
+    def forward(self, stream=None):
+        """The whole layer: the routing (of a layer built from logits), the
+        fused expert steps, the combine and the adapters (if it has any)."""
+        if self.logits is not None:
+            self.route(stream)
+        self.run_fused(stream)
+        self.combine(stream)
+        if self.adapters is not None:
+            self.apply_adapters(stream)
+
+    def backward(self, dout, stream=None, dloss=None):
+        """The gradient of the output (dout, float32 [T, hidden] on the device)
+        and of the balance loss (dloss, float32 [1], None for 1) -> dlogits."""
+        _steps.moe_combine_backward(self.dm[:self.rows], self.route_w, dout, self.dw, stream=stream)
+        _steps.moe_route_backward(self.logits, self.ids_dev, self.dw, self.dlogits, renorm=self.renorm,
+                                  seq_off=self.seq_off, coef=self.balance_coef,
+                                  counts=None if self.seq_off is None else self.counts, dloss=dloss,
+                                  stream=stream)
+        return self.dlogits
 
     def _buffer(self, name: str, shape, dtype):
         """An output buffer; with guards, a view into the middle of a larger

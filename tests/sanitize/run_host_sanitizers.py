@@ -3,9 +3,9 @@
 Builds, with gcc/g++ and -fsanitize=address,undefined (no GPU code is
 compiled here):
   * the C oracle (oracle/moe_oracle.c), and
-  * the host side of the library (csrc/moe_prefill.cpp: argument checks, host
-    plans, plan queries, the ABI's exports) linked with host_stubs.cpp in place
-    of the device launchers,
+  * the host side of the library (csrc/moe_prefill.cpp and csrc/moe_layer.cpp:
+    argument checks, host plans, plan queries, the ABI's exports) linked with
+    host_stubs.cpp and host_stubs_layer.cpp in place of the device launchers,
 into a temporary directory, then runs the CPU tests that exercise them (the
 oracle's pins and the host ABI tests) with the sanitizer runtime preloaded and
 MOE_ORACLE_LIB / MOE_PREFILL_LIB pointing the loaders at the instrumented
@@ -24,7 +24,8 @@ import tempfile
 ROOT = os.path.dirname(os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 SAN = ["-fsanitize=address,undefined", "-fno-sanitize-recover=all", "-fno-omit-frame-pointer", "-g"]
 TESTS = ["tests/test_oracle_q8_1.py", "tests/test_oracle_weights.py", "tests/test_oracle_products.py",
-         "tests/test_oracle_swiglu_plan.py", "tests/test_oracle_combine.py", "tests/test_abi_host.py"]
+         "tests/test_oracle_swiglu_plan.py", "tests/test_oracle_combine.py", "tests/test_abi_host.py",
+         "tests/test_layer_abi_host.py"]
 
 
 def main() -> int:
@@ -36,7 +37,9 @@ def main() -> int:
     subprocess.check_call(["g++", "-O1", "-std=c++17", "-fPIC", "-shared", *SAN, "-D__HIP_PLATFORM_AMD__",
                            "-I/opt/rocm/include",
                            os.path.join(ROOT, "quantized_moe_expert_scatter_amd", "csrc", "moe_prefill.cpp"),
+                           os.path.join(ROOT, "quantized_moe_expert_scatter_amd", "csrc", "moe_layer.cpp"),
                            os.path.join(ROOT, "tests", "sanitize", "host_stubs.cpp"),
+                           os.path.join(ROOT, "tests", "sanitize", "host_stubs_layer.cpp"),
                            "-o", host, "-L/opt/rocm/lib", "-lamdhip64", "-Wl,-rpath,/opt/rocm/lib"])
     for lib in (oracle, host):                     # both builds are instrumented
         syms = subprocess.check_output(["nm", "-D", lib], text=True)
