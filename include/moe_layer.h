@@ -39,6 +39,7 @@ enum { MOE_ROUTE_RENORM = 1 };
 #define MOE_ROUTE_MAX_EXPERTS 2048 /* as moe_prefill_plan_device */
 #define MOE_ROUTE_MAX_TOPK 64
 #define MOE_ADAPTER_MAX_RANK 256
+#define MOE_ADAPTER_MAX_TOKENS (1 << 24)
 
 /* The router's choice.  With p[t] the softmax of logits row t,
  *   ids[t*topk + k]  the expert of the k-th largest logit (equal logits: the
@@ -143,6 +144,7 @@ size_t moe_adapters_bytes(const moe_adapter_set *set, int tokens);
  *   out[t] = base[t] + scale[i] * b[i] * (a[i] * x[t]),   i = ids[t],
  * over the first ranks[i] rows of a[i] and columns of b[i]; a row whose id is
  * negative or >= n_adapter has no adapter: out[t] = base[t].
+ *   tokens at most 2^24
  *   ids    device int32 [tokens], in any order (rows of one request usually
  *          stand together: prompts; or every row its own: new tokens)
  *   x      device [tokens x n_in], base and out: device [tokens x n_out], rows

@@ -54,12 +54,43 @@ def lib() -> ctypes.CDLL:
     return _bound
 
 
+_torch = None
+_codes = {}
+
+
+def _load_torch():
+    """torch, imported on first use like the library."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+        _codes.update({torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16})
+    return _torch
+
+
 def _dtype(t, what: str) -> int:
-    import torch
-    code = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}.get(t.dtype)
+    _load_torch()
+    code = _codes.get(t.dtype)
     if code is None:
         raise MoeError(-3, f"{what}: {t.dtype}")
     return code
+
+
+def _stream(stream):
+    """The raw stream, torch's current one by default."""
+    if stream is None:
+        c = _load_torch()._C
+        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
+    return _lib._stream(stream)
+
+
+def _address(t, what: str):
+    device = t.get_device()
+    if device < 0 or not t.is_cuda:
+        raise MoeError(-1, f"{what}: on {t.device}, not in device memory")
+    if device != _load_torch()._C._cuda_getDevice():
+        raise MoeError(-1, f"{what}: on {t.device}, the current device is cuda:{_load_torch()._C._cuda_getDevice()}")
+    return t.data_ptr()
 
 
 def _arg(t, what: str, dtype, shape):
@@ -68,27 +99,17 @@ def _arg(t, what: str, dtype, shape):
         return None
     if t.dtype != dtype:
         raise MoeError(-3, f"{what}: {t.dtype} instead of {dtype}")
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.shape != shape or not t.is_contiguous():
         raise MoeError(-1, f"{what}: shape {tuple(t.shape)}, strides {t.stride()}; dense {tuple(shape)} wanted")
     return _address(t, what)
 
 
 def _rows(t, what: str, shape):
     """A matrix with dense rows -> its address and row stride in elements."""
-    if tuple(t.shape) != tuple(shape) or (t.dim() == 2 and t.shape[1] > 1 and t.stride(1) != 1):
+    if t.shape != shape or (t.stride(1) != 1 and shape[1] > 1):
         raise MoeError(-1, f"{what}: shape {tuple(t.shape)}, strides {t.stride()}; {tuple(shape)} with dense rows wanted")
     # the stride of a single row says nothing: torch may give it any value
-    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
-    return _address(t, what), ld
-
-
-def _address(t, what: str):
-    import torch
-    if not t.is_cuda:
-        raise MoeError(-1, f"{what}: on {t.device}, not in device memory")
-    if t.device.index != torch.cuda.current_device():
-        raise MoeError(-1, f"{what}: on {t.device}, the current device is {torch.cuda.current_device()}")
-    return t.data_ptr()
+    return _address(t, what), t.stride(0) if shape[0] > 1 else shape[1]
 
 
 def _out_of_place(t, what: str):
@@ -100,8 +121,8 @@ def _out_of_place(t, what: str):
 def _route(logits, topk: int, renorm: bool, scale: float):
     if logits.dim() != 2:
         raise MoeError(-1, f"logits: shape {tuple(logits.shape)}")
-    ptr, ld = _rows(logits, "logits", logits.shape)
     T, E = logits.shape
+    ptr, ld = _rows(logits, "logits", (T, E))
     return (ptr, ld, _dtype(logits, "logits"), T, E, topk, MOE_ROUTE_RENORM if renorm else 0, scale)
 
 
@@ -113,11 +134,11 @@ def _matrix(t, what: str):
 
 def moe_route(logits, ids, w, renorm: bool = True, scale: float = 1.0, stream=None):
     """logits [T, E] (fp32, bf16 or fp16, dense rows) -> ids int32 [T, topk], w fp32 [T, topk]."""
-    import torch
+    torch = _load_torch()
     T, K = _matrix(ids, "ids")
     head = _route(logits, K, renorm, scale)
     _lib._check(lib().moe_route(*head, _arg(ids, "ids", torch.int32, (head[3], K)),
-                                _arg(w, "w", torch.float32, (head[3], K)), _lib._stream(stream)), "moe_route")
+                                _arg(w, "w", torch.float32, (head[3], K)), _stream(stream)), "moe_route")
 
 
 def moe_balance_bytes(tokens: int, n_expert: int, n_seq: int) -> int:
@@ -128,7 +149,7 @@ def moe_route_balance(logits, seq_off, coef: float, ids, w, counts, probs, loss,
                       renorm: bool = True, scale: float = 1.0, stream=None):
     """moe_route with the balance statistics of the sequences seq_off (int32 [S+1]) bounds:
     counts int32 [S, E], probs fp32 [S, E], loss fp32 [1]."""
-    import torch
+    torch = _load_torch()
     T, K = _matrix(ids, "ids")
     head = _route(logits, K, renorm, scale)
     T, E, S = head[3], head[4], seq_off.numel() - 1
@@ -137,7 +158,7 @@ def moe_route_balance(logits, seq_off, coef: float, ids, w, counts, probs, loss,
         *head, _arg(seq_off, "seq_off", i32, (S + 1,)), S, coef, _arg(ids, "ids", i32, (T, K)),
         _arg(w, "w", f32, (T, K)), _arg(counts, "counts", i32, (S, E)), _arg(probs, "probs", f32, (S, E)),
         _arg(loss, "loss", f32, (1,)), _address(workspace, "workspace"),
-        workspace.numel() * workspace.element_size(), _lib._stream(stream)), "moe_route_balance")
+        workspace.numel() * workspace.element_size(), _stream(stream)), "moe_route_balance")
 
 
 def moe_route_backward(logits, ids, dw, dlogits, renorm: bool = True, scale: float = 1.0, seq_off=None,
@@ -145,7 +166,7 @@ def moe_route_backward(logits, ids, dw, dlogits, renorm: bool = True, scale: flo
     """The gradient of moe_route / moe_route_balance: dw fp32 [T, topk] (or None) and the loss's
     (seq_off and counts of the forward call, dloss fp32 [1] or None for 1) -> dlogits, the
     logits' type and shape."""
-    import torch
+    torch = _load_torch()
     T, K = _matrix(ids, "ids")
     head = _route(logits, K, renorm, scale)
     T, E = head[3], head[4]
@@ -158,14 +179,13 @@ def moe_route_backward(logits, ids, dw, dlogits, renorm: bool = True, scale: flo
     _lib._check(lib().moe_route_backward(
         *head, _arg(ids, "ids", i32, (T, K)), _arg(dw, "dw", f32, (T, K)),
         _arg(seq_off, "seq_off", i32, (S + 1,)), S, coef, _arg(counts, "counts", i32, (S, E)),
-        _arg(dloss, "dloss", f32, (1,)), d_ptr, ldd, _lib._stream(stream)), "moe_route_backward")
+        _arg(dloss, "dloss", f32, (1,)), d_ptr, ldd, _stream(stream)), "moe_route_backward")
 
 
 def moe_combine_backward(dm, w, dout, dw, ddm=None, stream=None):
     """The gradient of moe_combine: dout fp32 [T, H] -> dw fp32 [T, topk] and ddm fp32
     [T*topk, H] (either may be None; dm is read for dw, w [T, topk] for ddm)."""
-    import torch
-    f32 = torch.float32
+    f32 = _load_torch().float32
     T, H = _matrix(dout, "dout")
     of = dw if dw is not None else w
     if of is None:
@@ -173,7 +193,7 @@ def moe_combine_backward(dm, w, dout, dw, ddm=None, stream=None):
     K = _matrix(of, "dw" if dw is not None else "w")[1]
     _lib._check(lib().moe_combine_backward(
         _arg(dm, "dm", f32, (T * K, H)), _arg(w, "w", f32, (T, K)), _arg(dout, "dout", f32, (T, H)),
-        T, K, H, _arg(dw, "dw", f32, (T, K)), _arg(ddm, "ddm", f32, (T * K, H)), _lib._stream(stream)),
+        T, K, H, _arg(dw, "dw", f32, (T, K)), _arg(ddm, "ddm", f32, (T * K, H)), _stream(stream)),
         "moe_combine_backward")
 
 
@@ -183,7 +203,7 @@ class AdapterSet:
     [n], rank int32 [n] with each adapter's own rank (None: all full)."""
 
     def __init__(self, a, b, scale, rank=None):
-        import torch
+        torch = _load_torch()
         if a.dim() != 3 or b.dim() != 3:
             raise MoeError(-1, f"AdapterSet: a {tuple(a.shape)}, b {tuple(b.shape)}")
         n, r, n_in = a.shape
@@ -205,7 +225,8 @@ def moe_adapters_bytes(adapters: AdapterSet, tokens: int) -> int:
 def moe_adapters(adapters: AdapterSet, ids, x, base, out, workspace, stream=None):
     """out = base + each row's adapter over x: ids int32 [T] (negative: none), x [T, n_in], base
     and out [T, n_out] of fp32 or the set's type, dense rows; out may be base."""
-    import torch
+    torch = _load_torch()
+    _address(adapters.tensors[0], "adapters")
     T = ids.numel()
     x_ptr, ldx = _rows(x, "x", (T, adapters.n_in))
     b_ptr, ldb = _rows(base, "base", (T, adapters.n_out))
@@ -216,4 +237,4 @@ def moe_adapters(adapters: AdapterSet, ids, x, base, out, workspace, stream=None
     _lib._check(lib().moe_adapters(
         ctypes.byref(adapters.struct), _arg(ids, "ids", torch.int32, (T,)), T, _dtype(x, "x"), x_ptr, ldx,
         b_ptr, ldb, o_ptr, ldo, _address(workspace, "workspace"),
-        workspace.numel() * workspace.element_size(), _lib._stream(stream)), "moe_adapters")
+        workspace.numel() * workspace.element_size(), _stream(stream)), "moe_adapters")

@@ -1,8 +1,10 @@
 // adapter_kernels.hip -- low-rank adapters of many requests beside a shared
 // projection: out[t] = base[t] + scale[i] * b[i] * (a[i] * x[t]), i = ids[t].
 //
-// Two launches: the rows' low-rank values h = a[i] * x[t] (fp32, in the
-// workspace), then the update of the output rows.
+// Few rows take one launch: a workgroup has one row and a slice of its
+// outputs, and computes the row's low-rank values h = a[i] * x[t] itself.
+// More rows take two: the rows' h (fp32, in the workspace), then the update of
+// the output rows.
 #include "layer_ops.h"
 #include "wave.cuh"
 
@@ -15,6 +17,13 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
+// The single launch computes a row's h in each of its output slices, so it is
+// taken while tokens * rank * slices is small.  Measured at 2560 -> 2560 (3
+// slices) against the two launches, rows of one adapter / every row its own:
+// rank 16, 128 rows 7.0 / 8.3 us against 9.7 / 21.7; rank 64, 64 rows 11.3 /
+// 16.0 against 12.0 / 20; 128 rows 20.5 / 29.0 against 12.1 / 27.5.
+constexpr int kFewRows = 256;
+constexpr int kFewValues = 12288;
 
 // Eight elements of a row, 16-byte aligned.
 template <int DT>
@@ -34,55 +43,390 @@ __device__ __forceinline__ int rank_of(const AdapterArgs &g, int i) {
     return g.ranks ? min(max(g.ranks[i], 0), g.rank) : g.rank;
 }
 
-// One wave per (row, rank row): their dot over n_in.
-template <int XT, int WT>
-__global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterArgs g) {
-    const int lane = threadIdx.x & 63;
-    const int64_t waves = int64_t(gridDim.x) * (kThreads / 64);
-    for (int64_t job = int64_t(blockIdx.x) * (kThreads / 64) + (threadIdx.x >> 6);
-         job < int64_t(g.tokens) * g.rank; job += waves) {
-        const int64_t t = job / g.rank;
-        const int r = int(job % g.rank);
-        const int i = adapter_of(g, t);
-        if (i < 0 || r >= rank_of(g, i)) continue;
-        float sum = 0.0f;
-        for (int k = lane * 8; k < g.n_in; k += 512) {
-            float x[8], a[8];
-            load8<XT>(g.x, t * g.ldx + k, x);
-            load8<WT>(g.a, (int64_t(i) * g.rank + r) * g.n_in + k, a);
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kRowThreads = 1024;
+constexpr int kRowWaves = kRowThreads / 64;
+
+// One workgroup per (row, 1024 outputs).  h: each wave takes every 16th rank
+// row, RW of them at most, and passes over the row of x once; the outputs:
+// one per thread, its row of b (16-byte runs) against h from LDS.
+template <int XT, int WT, int RW>
+__global__ __launch_bounds__(kRowThreads) void adapter_row_kernel(AdapterArgs g, int slices) {
+    using T = typename Elem<XT>::T;
+    __shared__ float h[RW * kRowWaves];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t t = blockIdx.x / slices;
+    const int n = int(blockIdx.x % slices) * kRowThreads + int(threadIdx.x);
+    const bool live = n < g.n_out;
+    const int i = adapter_of(g, t);
+    T *out = static_cast<T *>(g.out) + t * g.ldo + n;
+    const T base = live ? static_cast<const T *>(g.base)[t * g.ldb + n] : T(0);
+    if (i < 0) {
+        if (live && g.out != g.base) *out = base;
+        return;
+    }
+    const int rank = rank_of(g, i);
+    // every address is clamped instead of skipped, so that the loads of several
+    // rank rows are in flight together; values past the ends are 0 or not used
+    constexpr int kGroup = RW < 2 ? RW : 2;
+    const int mine = (rank - wave + kRowWaves - 1) / kRowWaves;     // rank rows of this wave
+    // the output's row of b, on its way while h is computed
+    constexpr int kRuns = RW * kRowWaves / 8 < 8 ? RW * kRowWaves / 8 : 8;
+    const uint16_t *b_row = static_cast<const uint16_t *>(g.b) + (int64_t(i) * g.n_out + min(n, g.n_out - 1)) * g.rank;
+    u32x4 b_run[kRuns];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(x[j], a[j], sum);
+    for (int q = 0; q < kRuns; ++q)
+        b_run[q] = *reinterpret_cast<const u32x4 *>(b_row + min(q * 8, g.rank - 8));
+    const uint16_t *mat = static_cast<const uint16_t *>(g.a) + int64_t(i) * g.rank * g.n_in;
+    float sum[RW];
+#pragma unroll
+    for (int q = 0; q < RW; ++q) sum[q] = 0.0f;
+#pragma unroll (RW < 4 ? 5 / RW : 2)
+    for (int k = lane * 8; k - lane * 8 < g.n_in; k += 512) {
+        const int kc = min(k, g.n_in - 8);
+        float x[8];
+        load8<XT>(g.x, t * g.ldx + kc, x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = k < g.n_in ? x[j] : 0.0f;
+#pragma unroll
+        for (int q0 = 0; q0 < RW; q0 += kGroup)
+            if (q0 < mine) {
+                float a[kGroup][8];
+#pragma unroll
+                for (int q = 0; q < kGroup; ++q)
+                    load8<WT>(mat, int64_t(min((q0 + q) * kRowWaves + wave, rank - 1)) * g.n_in + kc, a[q]);
+#pragma unroll
+                for (int q = 0; q < kGroup; ++q)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sum[q0 + q] = __builtin_fmaf(x[j], a[q][j], sum[q0 + q]);
+            }
+    }
+#pragma unroll
+    for (int q = 0; q < RW; ++q) {
+        const float s = wave_sum(sum[q]);
+        if (lane == 0) h[q * kRowWaves + wave] = s;
+    }
+    __syncthreads();
+    if (!live) return;
+    float acc = 0.0f;
+    auto add = [&](u32x4 run, int r) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint16_t e = uint16_t(run[j / 2] >> (j % 2 * 16));
+            if (r + j < rank) acc = __builtin_fmaf(h[r + j], to_float<WT>(e), acc);
         }
-        sum = wave_sum(sum);
-        if (lane == 0) g.ws[job] = sum;
+    };
+#pragma unroll
+    for (int q = 0; q < kRuns; ++q)
+        if (q * 8 < rank) add(b_run[q], q * 8);
+    if constexpr (RW * kRowWaves > kRuns * 8)
+#pragma unroll 4
+        for (int r = kRuns * 8; r < rank; r += 8) add(*reinterpret_cast<const u32x4 *>(b_row + r), r);
+    *out = from_float<XT>(__builtin_fmaf(g.scale[i], acc, to_float<XT>(base)));
+}
+
+// Eight fp32 values as N bf16 vectors whose sum they are: each takes the next
+// eight bits of the mantissa (by truncation, so the rest is exact), three hold
+// all 24.  The matrix unit then multiplies fp32 values by bf16 ones with fp32
+// accuracy in three passes.  An infinity becomes NaN.
+template <int N>
+__device__ __forceinline__ void split(const float (&f)[8], u32x4 (&p)[N]) {
+    float rest[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) rest[j] = f[j];
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            p[q][j] = __builtin_amdgcn_perm(__float_as_uint(rest[2 * j + 1]), __float_as_uint(rest[2 * j]),
+                                            0x07060302u);
+        if (q + 1 < N)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                rest[j] = rest[j] - __uint_as_float(__float_as_uint(rest[j]) & 0xffff0000u);
     }
 }
 
-// One thread per output element.
-template <int XT, int WT>
-__global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterArgs g) {
+__device__ __forceinline__ f32x4 mfma_bf16(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
+                                                   0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mfma_f16(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
+                                                  0, 0);
+}
+
+// A 16-byte run of an adapter matrix as bf16 vectors: itself, or fp16 in two
+// (11 bits in 8 + 3).
+template <int WT> struct Weight {
+    static constexpr int kParts = WT == kBF16 ? 1 : 2;
+    u32x4 p[kParts];
+    __device__ __forceinline__ void set(u32x4 raw) {
+        if constexpr (WT == kBF16) {
+            p[0] = raw;
+        } else {
+            const f16x8 h = __builtin_bit_cast(f16x8, raw);
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = float(h[j]);
+            split<2>(f, p);
+        }
+    }
+};
+
+// c += w * v over bf16 parts, the smallest first; products below 2^-24 of the
+// largest (part indexes adding up to 3 or more) are left out.
+template <int WP, int VP>
+__device__ __forceinline__ f32x4 mfma_parts(const u32x4 (&w)[WP], const u32x4 (&v)[VP], f32x4 c) {
+#pragma unroll
+    for (int s = WP + VP - 2; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i < WP; ++i)
+            if (s - i >= 0 && s - i < VP && s < 3) c = mfma_bf16(w[i], v[s - i], c);
+    return c;
+}
+
+// Rows of a tile and their adapters, the same in every wave: lane l has row l.
+struct TileRows {
+    int id;               // this lane's row's adapter, -1: none (or no such row)
+    uint64_t left;        // rows not handled yet
+    __device__ __forceinline__ TileRows(const AdapterArgs &g, int64_t first, int rows, int lane) {
+        id = lane < rows && first + lane < g.tokens ? adapter_of(g, first + lane) : -1;
+        left = __ballot(id >= 0);
+    }
+    // The next adapter of the tile, -1 at the end.
+    __device__ __forceinline__ int next() {
+        if (left == 0) return -1;
+        const int a = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)left) - 1);
+        left &= ~__ballot(id == a);
+        return a;
+    }
+};
+
+// h for a tile of 16 * MR rows, 16 * NR rank rows and a slice of n_in: the
+// four waves take 32 values in turn and are added through LDS.  A tile with
+// rows of several adapters passes over x once for each; gridDim.z workgroups
+// share those passes.  The matrix unit's rows are rank rows, its columns rows
+// of x, so whatever a row holds stays in its column.
+template <int XT, int WT, int NR, int MR>
+__global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterArgs g, AdapterSplit s) {
+    constexpr int kXP = XT == kF32 ? 3 : 1;
+    __shared__ f32x4 red[4][NR][MR][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t first = int64_t(blockIdx.x / s.splits) * (16 * MR);
+    const int plane = int(blockIdx.x % s.splits);
+    const int r0 = int(blockIdx.y) * 16 * NR;
+    const int k0 = plane * s.slice + wave * 32 + (lane >> 4) * 8;
+    const int k1 = min(g.n_in, (plane + 1) * s.slice);
+    TileRows rows(g, first, 16 * MR, lane);
+    int64_t x_at[MR];
+#pragma unroll
+    for (int m = 0; m < MR; ++m) {
+        const int64_t t = first + m * 16 + (lane & 15);
+        x_at[m] = (t < g.tokens ? t : g.tokens - 1) * g.ldx;
+    }
+    for (int pass = 0, a; (a = rows.next()) >= 0; ++pass) {
+        if (pass % int(gridDim.z) != int(blockIdx.z)) continue;
+        const int rank = rank_of(g, a);
+        if (r0 >= rank) continue;
+        const uint16_t *mat = static_cast<const uint16_t *>(g.a) + int64_t(a) * g.rank * g.n_in;
+        const uint16_t *a_row[NR];
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+            a_row[n] = mat + int64_t(min(r0 + n * 16 + (lane & 15), rank - 1)) * g.n_in;
+        f32x4 acc[NR][MR];
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int m = 0; m < MR; ++m) acc[n][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        const u32x4 zero = {0, 0, 0, 0};
+        for (int k = k0; k - (lane >> 4) * 8 < k1; k += kAdapterStep) {
+            const bool in = k < k1;
+            const int kc = in ? k : 0;
+            u32x4 w_raw[NR];
+#pragma unroll
+            for (int n = 0; n < NR; ++n) w_raw[n] = *reinterpret_cast<const u32x4 *>(a_row[n] + kc);
+            u32x4 v[MR][kXP];
+#pragma unroll
+            for (int m = 0; m < MR; ++m) {
+                if constexpr (XT == kF32) {
+                    float f[8];
+                    load8<kF32>(g.x, x_at[m] + kc, f);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) f[j] = in ? f[j] : 0.0f;
+                    split<3>(f, v[m]);
+                } else {
+                    v[m][0] = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(g.x) + x_at[m] + kc);
+                    v[m][0] = in ? v[m][0] : zero;
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                const u32x4 raw = in ? w_raw[n] : zero;
+                if constexpr (XT == kF16) {
+#pragma unroll
+                    for (int m = 0; m < MR; ++m) acc[n][m] = mfma_f16(raw, v[m][0], acc[n][m]);
+                } else {
+                    Weight<WT> w;
+                    w.set(raw);
+#pragma unroll
+                    for (int m = 0; m < MR; ++m) acc[n][m] = mfma_parts(w.p, v[m], acc[n][m]);
+                }
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int m = 0; m < MR; ++m) red[wave][n][m][lane] = acc[n][m];
+        __syncthreads();
+        for (int c = threadIdx.x; c < NR * MR * 64; c += kThreads) {
+            const int n = c / (MR * 64), m = c / 64 % MR, l = c & 63;
+            const f32x4 h = (red[0][n][m][l] + red[1][n][m][l]) + (red[2][n][m][l] + red[3][n][m][l]);
+            const int row = m * 16 + (l & 15), r = r0 + n * 16 + (l >> 4) * 4;
+            const int64_t t = first + row;
+            if (r < g.rank && t < g.tokens && adapter_of(g, t) == a)
+                *reinterpret_cast<f32x4 *>(g.ws + (int64_t(plane) * g.tokens + t) * g.rank + r) = h;
+        }
+        __syncthreads();
+    }
+}
+
+// The update of a tile of 16 * MR rows, 256 outputs at a time (64 per wave):
+// h, the planes added, stands in LDS; the matrix unit's rows are outputs, so
+// a lane gets four consecutive outputs of one row.  For 16-bit rows the
+// outputs of two tiles are dealt so that a lane has eight.
+constexpr int kUpRank = 64;          // rank values of h in LDS at a time
+constexpr int kUpStride = kUpRank + 4;
+
+template <int XT, int WT, int MR>
+__global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterArgs g, AdapterSplit s, int slices, int per) {
     using T = typename Elem<XT>::T;
-    const int64_t threads = int64_t(gridDim.x) * kThreads;
-    for (int64_t job = int64_t(blockIdx.x) * kThreads + threadIdx.x; job < int64_t(g.tokens) * g.n_out;
-         job += threads) {
-        const int64_t t = job / g.n_out;
-        const int n = int(job % g.n_out);
-        const T base = static_cast<const T *>(g.base)[t * g.ldb + n];
-        T *out = static_cast<T *>(g.out) + t * g.ldo + n;
-        const int i = adapter_of(g, t);
-        if (i < 0) {
-            if (g.out != g.base) *out = base;
+    constexpr int kHP = XT == kF32 ? 3 : 2;      // 16 bits of h are enough for 16-bit rows
+    constexpr int kRun = XT == kF32 ? 4 : 8;     // consecutive outputs of a lane
+    constexpr int kRuns = 16 / kRun;
+    __shared__ float h[16 * MR][kUpStride];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t first = int64_t(blockIdx.x / slices) * (16 * MR);
+    const int n_begin = int(blockIdx.x % slices) * per * kThreads;
+    const int n_end = min(g.n_out, n_begin + per * kThreads);
+    TileRows rows(g, first, 16 * MR, lane);
+    const bool others = blockIdx.z == 0 && g.out != g.base;
+    int id[MR];
+#pragma unroll
+    for (int m = 0; m < MR; ++m) id[m] = __shfl(rows.id, m * 16 + (lane & 15));
+    // the output of register i of tile j in this lane: o + (j * 4 / kRun) * (4 * kRun) + (j * 4 % kRun) + i,
+    // with lane group q at q * kRun; the matrix row m of tile j is the same with q = m / 4, i = m % 4
+    auto out_of = [](int j, int q) { return (j * 4 / kRun) * (4 * kRun) + q * kRun + (j * 4) % kRun; };
+    for (int pass = -1, a = -1;; ++pass) {
+        if (pass >= 0) {
+            a = rows.next();
+            if (a < 0) break;
+            if (pass % int(gridDim.z) != int(blockIdx.z)) continue;
+        } else if (!others) {
             continue;
         }
-        const int rank = rank_of(g, i);
-        float sum = 0.0f;
-        for (int r = 0; r < rank; r += 8) {
-            float b[8];
-            load8<WT>(g.b, (int64_t(i) * g.n_out + n) * g.rank + r, b);
-            for (int j = 0; j < 8 && r + j < rank; ++j)
-                sum = __builtin_fmaf(g.ws[t * g.rank + r + j], b[j], sum);
+        // pass -1: the rows without an adapter, copied
+        const int rank = a < 0 ? 0 : rank_of(g, a);
+        const float scale = a < 0 ? 0.0f : g.scale[a];
+        const uint16_t *mat = static_cast<const uint16_t *>(g.b) + int64_t(max(a, 0)) * g.n_out * g.rank;
+        if (a < 0) {
+            bool any = false;
+#pragma unroll
+            for (int m = 0; m < MR; ++m) any |= id[m] < 0 && first + m * 16 + (lane & 15) < g.tokens;
+            if (!__any(any)) continue;
         }
-        *out = from_float<XT>(__builtin_fmaf(g.scale[i], sum, to_float<XT>(base)));
+        const bool one_block = rank <= kUpRank;
+        auto stage = [&](int b) {
+            __syncthreads();
+            for (int c = threadIdx.x; c < 16 * MR * (kUpRank / 4); c += kThreads) {
+                const int row = c / (kUpRank / 4), r = b + c % (kUpRank / 4) * 4;
+                const int64_t t = first + row;
+                f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (r < rank && t < g.tokens && adapter_of(g, t) == a) {
+                    for (int q = 0; q < s.splits; ++q)
+                        v += *reinterpret_cast<const f32x4 *>(g.ws + (int64_t(q) * g.tokens + t) * g.rank + r);
+                    for (int i = 0; i < 4; ++i) v[i] = r + i < rank ? v[i] : 0.0f;
+                }
+                *reinterpret_cast<f32x4 *>(&h[row][r - b]) = v;
+            }
+            __syncthreads();
+        };
+        if (one_block && rank > 0) stage(0);
+        for (int n0 = n_begin; n0 < n_end; n0 += kThreads) {
+            const int o = n0 + wave * 64;
+            f32x4 acc[4][MR];
+            T base[MR][16];
+            struct alignas(16) Run { T e[kRun]; };
+#pragma unroll
+            for (int m = 0; m < MR; ++m) {
+                const int64_t t = first + m * 16 + (lane & 15);
+#pragma unroll
+                for (int q = 0; q < kRuns; ++q) {
+                    const int n = o + q * (4 * kRun) + (lane >> 4) * kRun;
+                    Run b{};
+                    if (n < n_end && t < g.tokens && id[m] == a)
+                        b = *reinterpret_cast<const Run *>(static_cast<const T *>(g.base) + t * g.ldb + n);
+#pragma unroll
+                    for (int i = 0; i < kRun; ++i) base[m][q * kRun + i] = b.e[i];
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[j][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            }
+            for (int b = 0; b < rank; b += kUpRank) {
+                if (!one_block) stage(b);
+                for (int k = b; k < min(rank, b + kUpRank); k += 32) {
+                    const int kl = k + (lane >> 4) * 8;
+                    u32x4 v[MR][kHP];
+#pragma unroll
+                    for (int m = 0; m < MR; ++m) {
+                        float f[8];
+                        const float *src = &h[m * 16 + (lane & 15)][kl - b];
+                        *reinterpret_cast<f32x4 *>(f) = *reinterpret_cast<const f32x4 *>(src);
+                        *reinterpret_cast<f32x4 *>(f + 4) = *reinterpret_cast<const f32x4 *>(src + 4);
+                        split<kHP>(f, v[m]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int n = min(o + out_of(j, (lane & 15) >> 2) + (lane & 3), g.n_out - 1);
+                        u32x4 raw = *reinterpret_cast<const u32x4 *>(mat + int64_t(n) * g.rank +
+                                                                     min(kl, g.rank - 8));
+                        // columns past the adapter's rank are not part of it, whatever they hold
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int k2 = kl + 2 * i;
+                            raw[i] = k2 + 1 < rank ? raw[i] : (k2 < rank ? raw[i] & 0xffffu : 0u);
+                        }
+                        Weight<WT> w;
+                        w.set(raw);
+#pragma unroll
+                        for (int m = 0; m < MR; ++m) acc[j][m] = mfma_parts(w.p, v[m], acc[j][m]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < MR; ++m) {
+                const int64_t t = first + m * 16 + (lane & 15);
+                if (t >= g.tokens || id[m] != a) continue;
+#pragma unroll
+                for (int q = 0; q < kRuns; ++q) {
+                    const int n = o + q * (4 * kRun) + (lane >> 4) * kRun;
+                    if (n >= n_end) continue;
+                    Run r;
+#pragma unroll
+                    for (int i = 0; i < kRun; ++i) {
+                        const int c = q * kRun + i;
+                        r.e[i] = a < 0 ? base[m][c]
+                                       : from_float<XT>(__builtin_fmaf(scale, acc[c / 4][m][c % 4],
+                                                                       to_float<XT>(base[m][c])));
+                    }
+                    *reinterpret_cast<Run *>(static_cast<T *>(g.out) + t * g.ldo + n) = r;
+                }
+            }
+        }
     }
 }
 
@@ -99,15 +443,57 @@ hipError_t by_types(const AdapterArgs &g, F f) {
 
 hipError_t launch_adapters(const AdapterArgs &g, hipStream_t stream) {
     return by_types(g, [&](auto XT, auto WT) {
-        auto groups = [](int64_t n) { return dim3(unsigned(n < 65536 ? n : 65536)); };
-        hipLaunchKernelGGL((adapter_down_kernel<XT.value, WT.value>),
-                           groups((int64_t(g.tokens) * g.rank + 3) / 4), dim3(kThreads), 0, stream, g);
-        const hipError_t err = hipGetLastError();
-        if (err != hipSuccess) return err;
-        hipLaunchKernelGGL((adapter_up_kernel<XT.value, WT.value>),
-                           groups((int64_t(g.tokens) * g.n_out + kThreads - 1) / kThreads), dim3(kThreads),
-                           0, stream, g);
-        return hipGetLastError();
+        const int slices = (g.n_out + kRowThreads - 1) / kRowThreads;
+        if (g.tokens <= kFewRows && int64_t(g.tokens) * g.rank * slices <= kFewValues) {
+            const dim3 grid(unsigned(g.tokens) * unsigned(slices));
+            if (g.rank <= 16)
+                hipLaunchKernelGGL((adapter_row_kernel<XT.value, WT.value, 1>), grid, dim3(kRowThreads), 0,
+                                   stream, g, slices);
+            else if (g.rank <= 32)
+                hipLaunchKernelGGL((adapter_row_kernel<XT.value, WT.value, 2>), grid, dim3(kRowThreads), 0,
+                                   stream, g, slices);
+            else if (g.rank <= 64)
+                hipLaunchKernelGGL((adapter_row_kernel<XT.value, WT.value, 4>), grid, dim3(kRowThreads), 0,
+                                   stream, g, slices);
+            else
+                hipLaunchKernelGGL((adapter_row_kernel<XT.value, WT.value, 16>), grid, dim3(kRowThreads), 0,
+                                   stream, g, slices);
+            return hipGetLastError();
+        }
+        const AdapterSplit s = adapter_split(g.tokens, g.n_in);
+        auto passes = [](int64_t groups) {
+            const int64_t n = 2048 / groups;
+            return unsigned(n < 1 ? 1 : n > 16 ? 16 : n);
+        };
+        auto down = [&](auto NR, auto MR) {
+            const unsigned blocks = unsigned((g.rank + 16 * NR.value - 1) / (16 * NR.value));
+            const dim3 grid(unsigned(s.tiles) * unsigned(s.splits), blocks, passes(int64_t(s.tiles) * s.splits));
+            hipLaunchKernelGGL((adapter_down_kernel<XT.value, WT.value, NR.value, MR.value>), grid, dim3(kThreads),
+                               0, stream, g, s);
+        };
+        auto up = [&](auto MR) {
+            const int all = (g.n_out + kThreads - 1) / kThreads;
+            int slices = int((2048 + int64_t(s.tiles) - 1) / s.tiles);
+            if (slices > all) slices = all;
+            const int per = (all + slices - 1) / slices;
+            slices = (all + per - 1) / per;
+            const dim3 grid(unsigned(s.tiles) * unsigned(slices), 1, passes(int64_t(s.tiles) * slices));
+            hipLaunchKernelGGL((adapter_up_kernel<XT.value, WT.value, MR.value>), grid, dim3(kThreads), 0, stream, g,
+                               s, slices, per);
+        };
+        using One = std::integral_constant<int, 1>;
+        using Two = std::integral_constant<int, 2>;
+        using Four = std::integral_constant<int, 4>;
+        auto both = [&](auto MR) {
+            if (g.rank <= 16) down(One{}, MR);
+            else if (g.rank <= 32) down(Two{}, MR);
+            else down(Four{}, MR);
+            const hipError_t err = hipGetLastError();
+            if (err != hipSuccess) return err;
+            up(MR);
+            return hipGetLastError();
+        };
+        return s.row_groups == 1 ? both(One{}) : both(Two{});
     });
 }
 

@@ -90,10 +90,30 @@ struct AdapterArgs {
     int64_t ldo;
     float *ws;
 };
-// The rows' low-rank values, fp32 [tokens][rank].
+// How the rows' low-rank values are computed: tiles of 16 * row_groups rows,
+// the contraction in `splits` slices of `slice` (a slice's values are a plane
+// of the workspace, fp32 [splits][tokens][rank], added where they are read).
+struct AdapterSplit {
+    int row_groups, tiles, splits, slice;
+};
+constexpr int kAdapterStep = 128;        // 4 waves x 32 values: what a slice is a multiple of
+constexpr int kAdapterGroups = 512;      // workgroups a launch should have, two per CU
+inline AdapterSplit adapter_split(int tokens, int n_in) {
+    AdapterSplit s{};
+    s.row_groups = tokens > 4096 ? 2 : 1;
+    s.tiles = int(((long long)tokens + 16 * s.row_groups - 1) / (16 * s.row_groups));
+    const int steps = (n_in + kAdapterStep - 1) / kAdapterStep;
+    int want = s.tiles > 0 ? (kAdapterGroups + s.tiles - 1) / s.tiles : 1;
+    if (want > 8) want = 8;
+    if (want > steps) want = steps;
+    const int per = (steps + want - 1) / want;
+    s.slice = per * kAdapterStep;
+    s.splits = (steps + per - 1) / per;
+    return s;
+}
 inline size_t adapter_workspace(int tokens, int rank, int n_in) {
-    (void)n_in;
-    return (size_t(tokens) * size_t(rank) * 4 + 15) & ~size_t(15);
+    const size_t planes = size_t(adapter_split(tokens, n_in).splits);
+    return (planes * size_t(tokens) * size_t(rank) * 4 + 15) & ~size_t(15);
 }
 hipError_t launch_adapters(const AdapterArgs &a, hipStream_t stream);
 

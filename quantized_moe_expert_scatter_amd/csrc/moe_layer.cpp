@@ -134,7 +134,7 @@ int moe_combine_backward(const float *dm, const float *w, const float *dout, int
 
 size_t moe_adapters_bytes(const moe_adapter_set *set, int tokens) {
     int st;
-    if (!valid_set(set, &st) || tokens < 0) return 0;
+    if (!valid_set(set, &st) || tokens < 0 || tokens > MOE_ADAPTER_MAX_TOKENS) return 0;
     return adapter_workspace(tokens, set->rank, set->n_in);
 }
 
@@ -148,7 +148,7 @@ int moe_adapters(const moe_adapter_set *set, const int32_t *ids, int tokens, int
         return MOE_EALIGN;
     if (dtype != MOE_F32 && dtype != set->dtype) return MOE_EFORMAT;
     const int64_t far = int64_t(1) << 40;
-    if (tokens < 0 || ldx < set->n_in || ldb < set->n_out || ldo < set->n_out || ldx > far ||
+    if (tokens < 0 || tokens > MOE_ADAPTER_MAX_TOKENS || ldx < set->n_in || ldb < set->n_out || ldo < set->n_out || ldx > far ||
         ldb > far || ldo > far)
         return MOE_EINVAL;
     if (ldx % 8 || ldb % 8 || ldo % 8) return MOE_EALIGN;

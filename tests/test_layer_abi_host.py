@@ -169,6 +169,7 @@ def adapters(set_kw=None, **kw):
     ({}, dict(dtype=2), EFORMAT), ({}, dict(dtype=5), EFORMAT), ({}, dict(tokens=-1), EINVAL),
     ({}, dict(ldx=56), EINVAL), ({}, dict(ldb=120), EINVAL), ({}, dict(ldo=120), EINVAL),
     ({}, dict(ldx=68), EALIGN), ({}, dict(ldb=132), EALIGN), ({}, dict(ldo=132), EALIGN),
+    ({}, dict(tokens=(1 << 24) + 1), EINVAL), ({}, dict(tokens=1 << 24, nb=16), ESIZE),
     ({}, dict(ids=None), EINVAL), ({}, dict(x=None), EINVAL), ({}, dict(base=None), EINVAL),
     ({}, dict(out=None), EINVAL), ({}, dict(ws=None), EINVAL), ({}, dict(out=P, ldo=128), EINVAL),
     ({}, dict(out=2 * P, ldo=256), EINVAL), ({}, dict(nb=4 * 16 * 4 - 1), ESIZE)]
