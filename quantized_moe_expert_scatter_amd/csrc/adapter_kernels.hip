@@ -35,6 +35,21 @@ __device__ __forceinline__ void load8(const void *p, int64_t at, float (&f)[8]) 
     for (int j = 0; j < 8; ++j) f[j] = to_float<DT>(r.e[j]);
 }
 
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+// 16 bytes that are used once: past the caches.
+template <class R>
+__device__ __forceinline__ R stream_load(const void *p) {
+    return __builtin_bit_cast(R, __builtin_nontemporal_load(static_cast<const u32x4 *>(p)));
+}
+template <class R>
+__device__ __forceinline__ void stream_store(void *p, const R &r) {
+    __builtin_nontemporal_store(__builtin_bit_cast(u32x4, r), static_cast<u32x4 *>(p));
+}
+
 __device__ __forceinline__ int adapter_of(const AdapterArgs &g, int64_t t) {
     const int i = g.ids[t];
     return i >= 0 && i < g.n_adapter ? i : -1;
@@ -42,11 +57,6 @@ __device__ __forceinline__ int adapter_of(const AdapterArgs &g, int64_t t) {
 __device__ __forceinline__ int rank_of(const AdapterArgs &g, int i) {
     return g.ranks ? min(max(g.ranks[i], 0), g.rank) : g.rank;
 }
-
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kRowThreads = 1024;
 constexpr int kRowWaves = kRowThreads / 64;
@@ -243,30 +253,40 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterArgs g, A
         for (int n = 0; n < NR; ++n)
 #pragma unroll
             for (int m = 0; m < MR; ++m) acc[n][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        const u32x4 zero = {0, 0, 0, 0};
-        for (int k = k0; k - (lane >> 4) * 8 < k1; k += kAdapterStep) {
-            const bool in = k < k1;
-            const int kc = in ? k : 0;
-            u32x4 w_raw[NR];
+        // raw loads of one step, in flight while the step before is multiplied
+        struct Step {
+            u32x4 w[NR], x[MR][XT == kF32 ? 2 : 1];
+        };
+        auto load = [&](Step &q, int k) {
+            const int kc = k < k1 ? k : 0;       // past the slice: some values, not used
 #pragma unroll
-            for (int n = 0; n < NR; ++n) w_raw[n] = *reinterpret_cast<const u32x4 *>(a_row[n] + kc);
+            for (int n = 0; n < NR; ++n) q.w[n] = *reinterpret_cast<const u32x4 *>(a_row[n] + kc);
+#pragma unroll
+            for (int m = 0; m < MR; ++m) {
+                using T = typename Elem<XT>::T;
+                const u32x4 *src = reinterpret_cast<const u32x4 *>(static_cast<const T *>(g.x) + x_at[m] + kc);
+                q.x[m][0] = src[0];
+                if constexpr (XT == kF32) q.x[m][1] = src[1];
+            }
+        };
+        auto multiply = [&](const Step &q, int k) {
+            const bool in = k < k1;
+            const u32x4 zero = {0, 0, 0, 0};
             u32x4 v[MR][kXP];
 #pragma unroll
             for (int m = 0; m < MR; ++m) {
                 if constexpr (XT == kF32) {
                     float f[8];
-                    load8<kF32>(g.x, x_at[m] + kc, f);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) f[j] = in ? f[j] : 0.0f;
+                    for (int j = 0; j < 8; ++j) f[j] = in ? __uint_as_float(q.x[m][j / 4][j % 4]) : 0.0f;
                     split<3>(f, v[m]);
                 } else {
-                    v[m][0] = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(g.x) + x_at[m] + kc);
-                    v[m][0] = in ? v[m][0] : zero;
+                    v[m][0] = in ? q.x[m][0] : zero;
                 }
             }
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
-                const u32x4 raw = in ? w_raw[n] : zero;
+                const u32x4 raw = in ? q.w[n] : zero;
                 if constexpr (XT == kF16) {
 #pragma unroll
                     for (int m = 0; m < MR; ++m) acc[n][m] = mfma_f16(raw, v[m][0], acc[n][m]);
@@ -277,6 +297,16 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterArgs g, A
                     for (int m = 0; m < MR; ++m) acc[n][m] = mfma_parts(w.p, v[m], acc[n][m]);
                 }
             }
+        };
+        Step one, two;
+        load(one, k0);
+        const int steps = (k1 - (k0 - (lane >> 4) * 8) + kAdapterStep - 1) / kAdapterStep;
+        for (int q = 0; q < steps; q += 2) {
+            const int k = k0 + q * kAdapterStep;
+            load(two, k + kAdapterStep);
+            multiply(one, k);
+            load(one, k + 2 * kAdapterStep);
+            multiply(two, k + kAdapterStep);
         }
 #pragma unroll
         for (int n = 0; n < NR; ++n)
@@ -295,137 +325,182 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterArgs g, A
     }
 }
 
-// The update of a tile of 16 * MR rows, 256 outputs at a time (64 per wave):
-// h, the planes added, stands in LDS; the matrix unit's rows are outputs, so
-// a lane gets four consecutive outputs of one row.  For 16-bit rows the
-// outputs of two tiles are dealt so that a lane has eight.
+// The update of a tile of 16 * MR rows, 256 outputs at a time (64 per wave).
+// h, its planes added, stands in LDS; the matrix unit's rows are outputs, its
+// columns rows of the tile.  The 16 x 64 results pass through LDS so that base
+// and out move in whole row segments: 256 bytes of a row per 16 lanes reach
+// 6.2 TB/s in a copy of this shape, the 64 that the matrix unit's layout gives
+// 4.6.  KB: blocks of 32 rank values whose part of b is held in registers and
+// loaded while h is staged (0: any rank, 64 values at a time).
 constexpr int kUpRank = 64;          // rank values of h in LDS at a time
 constexpr int kUpStride = kUpRank + 4;
 
-template <int XT, int WT, int MR>
+template <int XT, int WT, int MR, int KB>
 __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterArgs g, AdapterSplit s, int slices, int per) {
     using T = typename Elem<XT>::T;
     constexpr int kHP = XT == kF32 ? 3 : 2;      // 16 bits of h are enough for 16-bit rows
-    constexpr int kRun = XT == kF32 ? 4 : 8;     // consecutive outputs of a lane
-    constexpr int kRuns = 16 / kRun;
+    constexpr int kRun = XT == kF32 ? 4 : 8;     // 16 bytes of a row
+    constexpr int kLanes = 64 / kRun;            // lanes of a row's 64 outputs
+    constexpr int kRows = 64 / kLanes;           // rows of one access
+    constexpr int kParts = 16 / kRows;           // accesses of 16 rows
+    struct alignas(16) Run { T e[kRun]; };
     __shared__ float h[16 * MR][kUpStride];
+    __shared__ float turn[4][16][64 + 4];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t first = int64_t(blockIdx.x / slices) * (16 * MR);
     const int n_begin = int(blockIdx.x % slices) * per * kThreads;
     const int n_end = min(g.n_out, n_begin + per * kThreads);
+    const T *base = static_cast<const T *>(g.base);
+    T *out = static_cast<T *>(g.out);
     TileRows rows(g, first, 16 * MR, lane);
-    const bool others = blockIdx.z == 0 && g.out != g.base;
-    int id[MR];
+    // this lane's share of an access: its rows' adapters and its column
+    const int col = wave * 64 + lane % kLanes * kRun;
+    int id[MR][kParts];
+    int64_t row[MR][kParts];
 #pragma unroll
-    for (int m = 0; m < MR; ++m) id[m] = __shfl(rows.id, m * 16 + (lane & 15));
-    // the output of register i of tile j in this lane: o + (j * 4 / kRun) * (4 * kRun) + (j * 4 % kRun) + i,
-    // with lane group q at q * kRun; the matrix row m of tile j is the same with q = m / 4, i = m % 4
-    auto out_of = [](int j, int q) { return (j * 4 / kRun) * (4 * kRun) + q * kRun + (j * 4) % kRun; };
-    for (int pass = -1, a = -1;; ++pass) {
-        if (pass >= 0) {
-            a = rows.next();
-            if (a < 0) break;
-            if (pass % int(gridDim.z) != int(blockIdx.z)) continue;
-        } else if (!others) {
-            continue;
-        }
-        // pass -1: the rows without an adapter, copied
-        const int rank = a < 0 ? 0 : rank_of(g, a);
-        const float scale = a < 0 ? 0.0f : g.scale[a];
-        const uint16_t *mat = static_cast<const uint16_t *>(g.b) + int64_t(max(a, 0)) * g.n_out * g.rank;
-        if (a < 0) {
-            bool any = false;
+    for (int m = 0; m < MR; ++m)
 #pragma unroll
-            for (int m = 0; m < MR; ++m) any |= id[m] < 0 && first + m * 16 + (lane & 15) < g.tokens;
-            if (!__any(any)) continue;
+        for (int i = 0; i < kParts; ++i) {
+            const int r = m * 16 + i * kRows + lane / kLanes;
+            id[m][i] = __shfl(rows.id, r);
+            row[m][i] = min(first + r, int64_t(g.tokens) - 1);
         }
-        const bool one_block = rank <= kUpRank;
+    Run b_run[MR][kParts];
+    auto load_base = [&](int n) {
+#pragma unroll
+        for (int m = 0; m < MR; ++m)
+#pragma unroll
+            for (int i = 0; i < kParts; ++i)
+                b_run[m][i] = stream_load<Run>(base + row[m][i] * g.ldb + min(n, g.n_out - kRun));
+    };
+    // rows without an adapter
+    if (blockIdx.z == 0 && g.out != g.base && __popcll(rows.left) < min(int64_t(16 * MR), g.tokens - first))
+        for (int n = n_begin + col; n < n_end; n += kThreads) {
+            load_base(n);
+#pragma unroll
+            for (int m = 0; m < MR; ++m)
+#pragma unroll
+                for (int i = 0; i < kParts; ++i)
+                    if (id[m][i] < 0 && first + m * 16 + i * kRows + lane / kLanes < g.tokens)
+                        stream_store(out + row[m][i] * g.ldo + n, b_run[m][i]);
+        }
+    for (int pass = 0, a; (a = rows.next()) >= 0; ++pass) {
+        if (pass % int(gridDim.z) != int(blockIdx.z)) continue;
+        const int rank = rank_of(g, a);
+        const float scale = g.scale[a];
+        const uint16_t *mat = static_cast<const uint16_t *>(g.b) + int64_t(a) * g.n_out * g.rank;
+        auto load_b = [&](int n0, int j, int k) {
+            const int n = min(n0 + wave * 64 + j * 16 + (lane & 15), g.n_out - 1);
+            return *reinterpret_cast<const u32x4 *>(mat + int64_t(n) * g.rank +
+                                                    min(k + (lane >> 4) * 8, g.rank - 8));
+        };
+        u32x4 w_run[KB > 0 ? KB : 1][4];
+        auto load_weights = [&](int n0) {
+            if constexpr (KB > 0)
+#pragma unroll
+                for (int q = 0; q < KB; ++q)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w_run[q][j] = load_b(n0, j, q * 32);
+        };
+        load_weights(n_begin);
+        load_base(n_begin + col);
         auto stage = [&](int b) {
             __syncthreads();
             for (int c = threadIdx.x; c < 16 * MR * (kUpRank / 4); c += kThreads) {
-                const int row = c / (kUpRank / 4), r = b + c % (kUpRank / 4) * 4;
-                const int64_t t = first + row;
+                const int r0 = c / (kUpRank / 4), r = b + c % (kUpRank / 4) * 4;
+                const int64_t t = first + r0;
                 f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-                if (r < rank && t < g.tokens && adapter_of(g, t) == a) {
-                    for (int q = 0; q < s.splits; ++q)
-                        v += *reinterpret_cast<const f32x4 *>(g.ws + (int64_t(q) * g.tokens + t) * g.rank + r);
-                    for (int i = 0; i < 4; ++i) v[i] = r + i < rank ? v[i] : 0.0f;
+                if (r < rank && t < g.tokens) {
+                    const float *src = g.ws + t * g.rank + r;
+                    const int64_t plane = int64_t(g.tokens) * g.rank;
+                    for (int q = 0; q < s.splits; q += 4) {
+                        f32x4 p[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            p[i] = *reinterpret_cast<const f32x4 *>(src + min(q + i, s.splits - 1) * plane);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (q + i < s.splits) v += p[i];
+                    }
                 }
-                *reinterpret_cast<f32x4 *>(&h[row][r - b]) = v;
+                // values past the rank, and rows of other adapters, may hold anything
+                const bool mine = t < g.tokens && adapter_of(g, t) == a;
+                for (int i = 0; i < 4; ++i) v[i] = mine && r + i < rank ? v[i] : 0.0f;
+                *reinterpret_cast<f32x4 *>(&h[r0][r - b]) = v;
             }
             __syncthreads();
         };
-        if (one_block && rank > 0) stage(0);
+        if (rank <= kUpRank) stage(0);
         for (int n0 = n_begin; n0 < n_end; n0 += kThreads) {
-            const int o = n0 + wave * 64;
             f32x4 acc[4][MR];
-            T base[MR][16];
-            struct alignas(16) Run { T e[kRun]; };
 #pragma unroll
-            for (int m = 0; m < MR; ++m) {
-                const int64_t t = first + m * 16 + (lane & 15);
-#pragma unroll
-                for (int q = 0; q < kRuns; ++q) {
-                    const int n = o + q * (4 * kRun) + (lane >> 4) * kRun;
-                    Run b{};
-                    if (n < n_end && t < g.tokens && id[m] == a)
-                        b = *reinterpret_cast<const Run *>(static_cast<const T *>(g.base) + t * g.ldb + n);
-#pragma unroll
-                    for (int i = 0; i < kRun; ++i) base[m][q * kRun + i] = b.e[i];
-                }
+            for (int m = 0; m < MR; ++m)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) acc[j][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            }
-            for (int b = 0; b < rank; b += kUpRank) {
-                if (!one_block) stage(b);
-                for (int k = b; k < min(rank, b + kUpRank); k += 32) {
-                    const int kl = k + (lane >> 4) * 8;
-                    u32x4 v[MR][kHP];
+            auto multiply = [&](int b, int k, auto weight) {
+                u32x4 v[MR][kHP];
 #pragma unroll
-                    for (int m = 0; m < MR; ++m) {
-                        float f[8];
-                        const float *src = &h[m * 16 + (lane & 15)][kl - b];
-                        *reinterpret_cast<f32x4 *>(f) = *reinterpret_cast<const f32x4 *>(src);
-                        *reinterpret_cast<f32x4 *>(f + 4) = *reinterpret_cast<const f32x4 *>(src + 4);
-                        split<kHP>(f, v[m]);
-                    }
+                for (int m = 0; m < MR; ++m) {
+                    float f[8];
+                    const float *src = &h[m * 16 + (lane & 15)][k - b + (lane >> 4) * 8];
+                    *reinterpret_cast<f32x4 *>(f) = *reinterpret_cast<const f32x4 *>(src);
+                    *reinterpret_cast<f32x4 *>(f + 4) = *reinterpret_cast<const f32x4 *>(src + 4);
+                    split<kHP>(f, v[m]);
+                }
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int n = min(o + out_of(j, (lane & 15) >> 2) + (lane & 3), g.n_out - 1);
-                        u32x4 raw = *reinterpret_cast<const u32x4 *>(mat + int64_t(n) * g.rank +
-                                                                     min(kl, g.rank - 8));
+                for (int j = 0; j < 4; ++j) {
+                    u32x4 raw = weight(j);
+                    if (k + 32 > rank) {
                         // columns past the adapter's rank are not part of it, whatever they hold
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const int k2 = kl + 2 * i;
-                            raw[i] = k2 + 1 < rank ? raw[i] : (k2 < rank ? raw[i] & 0xffffu : 0u);
+                            const int c = k + (lane >> 4) * 8 + 2 * i;
+                            raw[i] = c + 1 < rank ? raw[i] : (c < rank ? raw[i] & 0xffffu : 0u);
                         }
-                        Weight<WT> w;
-                        w.set(raw);
-#pragma unroll
-                        for (int m = 0; m < MR; ++m) acc[j][m] = mfma_parts(w.p, v[m], acc[j][m]);
                     }
+                    Weight<WT> w;
+                    w.set(raw);
+#pragma unroll
+                    for (int m = 0; m < MR; ++m) acc[j][m] = mfma_parts(w.p, v[m], acc[j][m]);
+                }
+            };
+            if constexpr (KB > 0) {
+#pragma unroll
+                for (int q = 0; q < KB; ++q)
+                    if (q * 32 < rank) multiply(0, q * 32, [&](int j) { return w_run[q][j]; });
+                if (n0 + kThreads < n_end) load_weights(n0 + kThreads);
+            } else {
+                for (int b = 0; b < rank; b += kUpRank) {
+                    if (rank > kUpRank) stage(b);
+                    for (int k = b; k < min(rank, b + kUpRank); k += 32)
+                        multiply(b, k, [&](int j) { return load_b(n0, j, k); });
                 }
             }
 #pragma unroll
             for (int m = 0; m < MR; ++m) {
-                const int64_t t = first + m * 16 + (lane & 15);
-                if (t >= g.tokens || id[m] != a) continue;
+                // results to rows: the wave's own part of LDS
+                __builtin_amdgcn_wave_barrier();
 #pragma unroll
-                for (int q = 0; q < kRuns; ++q) {
-                    const int n = o + q * (4 * kRun) + (lane >> 4) * kRun;
-                    if (n >= n_end) continue;
+                for (int j = 0; j < 4; ++j)
+                    *reinterpret_cast<f32x4 *>(&turn[wave][lane & 15][j * 16 + (lane >> 4) * 4]) = acc[j][m];
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                for (int i = 0; i < kParts; ++i) {
+                    const float *src = &turn[wave][i * kRows + lane / kLanes][lane % kLanes * kRun];
+                    float u[kRun];
+#pragma unroll
+                    for (int c = 0; c < kRun; c += 4)
+                        *reinterpret_cast<f32x4 *>(u + c) = *reinterpret_cast<const f32x4 *>(src + c);
                     Run r;
 #pragma unroll
-                    for (int i = 0; i < kRun; ++i) {
-                        const int c = q * kRun + i;
-                        r.e[i] = a < 0 ? base[m][c]
-                                       : from_float<XT>(__builtin_fmaf(scale, acc[c / 4][m][c % 4],
-                                                                       to_float<XT>(base[m][c])));
-                    }
-                    *reinterpret_cast<Run *>(static_cast<T *>(g.out) + t * g.ldo + n) = r;
+                    for (int c = 0; c < kRun; ++c)
+                        r.e[c] = from_float<XT>(__builtin_fmaf(scale, u[c], to_float<XT>(b_run[m][i].e[c])));
+                    if (id[m][i] == a && n0 + col < n_end) stream_store(out + row[m][i] * g.ldo + n0 + col, r);
                 }
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             }
+            if (n0 + kThreads < n_end) load_base(n0 + kThreads + col);
         }
     }
 }
@@ -461,6 +536,9 @@ hipError_t launch_adapters(const AdapterArgs &g, hipStream_t stream) {
             return hipGetLastError();
         }
         const AdapterSplit s = adapter_split(g.tokens, g.n_in);
+        using One = std::integral_constant<int, 1>;
+        using Two = std::integral_constant<int, 2>;
+        using Four = std::integral_constant<int, 4>;
         auto passes = [](int64_t groups) {
             const int64_t n = 2048 / groups;
             return unsigned(n < 1 ? 1 : n > 16 ? 16 : n);
@@ -475,15 +553,17 @@ hipError_t launch_adapters(const AdapterArgs &g, hipStream_t stream) {
             const int all = (g.n_out + kThreads - 1) / kThreads;
             int slices = int((2048 + int64_t(s.tiles) - 1) / s.tiles);
             if (slices > all) slices = all;
-            const int per = (all + slices - 1) / slices;
+            const int per = all / slices;               // rounded down: even shares, some more workgroups
             slices = (all + per - 1) / per;
             const dim3 grid(unsigned(s.tiles) * unsigned(slices), 1, passes(int64_t(s.tiles) * slices));
-            hipLaunchKernelGGL((adapter_up_kernel<XT.value, WT.value, MR.value>), grid, dim3(kThreads), 0, stream, g,
-                               s, slices, per);
+            auto go = [&](auto KB) {
+                hipLaunchKernelGGL((adapter_up_kernel<XT.value, WT.value, MR.value, KB.value>), grid,
+                                   dim3(kThreads), 0, stream, g, s, slices, per);
+            };
+            if (g.rank <= 32) go(One{});
+            else if (g.rank <= 64) go(Two{});
+            else go(std::integral_constant<int, 0>{});
         };
-        using One = std::integral_constant<int, 1>;
-        using Two = std::integral_constant<int, 2>;
-        using Four = std::integral_constant<int, 4>;
         auto both = [&](auto MR) {
             if (g.rank <= 16) down(One{}, MR);
             else if (g.rank <= 32) down(Two{}, MR);
