@@ -225,7 +225,11 @@ struct TileRows {
 template <int XT, int WT, int NR, int MR>
 __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterArgs g, AdapterSplit s) {
     constexpr int kXP = XT == kF32 ? 3 : 1;
-    __shared__ f32x4 red[4][NR][MR][64];
+    constexpr int kLoads = XT == kF32 ? 2 * MR : MR;     // 16-byte loads of x per lane and step
+    __shared__ union {
+        f32x4 red[4][NR][MR][64];
+        float x[XT == kF32 ? 4 : 1][16 * MR][36];
+    } lds;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t first = int64_t(blockIdx.x / s.splits) * (16 * MR);
     const int plane = int(blockIdx.x % s.splits);
@@ -233,11 +237,15 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterArgs g, A
     const int k0 = plane * s.slice + wave * 32 + (lane >> 4) * 8;
     const int k1 = min(g.n_in, (plane + 1) * s.slice);
     TileRows rows(g, first, 16 * MR, lane);
-    int64_t x_at[MR];
+    // x, 32 values of every row a step.  fp32: a load takes 8 rows' 128 bytes
+    // and the values turn through the wave's part of LDS; 16-bit: 16 rows' 64
+    // bytes, already in the matrix unit's layout.
+    const int kx = plane * s.slice + wave * 32 + (XT == kF32 ? (lane & 7) * 4 : (lane >> 4) * 8);
+    int64_t x_at[kLoads];
 #pragma unroll
-    for (int m = 0; m < MR; ++m) {
-        const int64_t t = first + m * 16 + (lane & 15);
-        x_at[m] = (t < g.tokens ? t : g.tokens - 1) * g.ldx;
+    for (int m = 0; m < kLoads; ++m) {
+        const int64_t t = first + (XT == kF32 ? m * 8 + (lane >> 3) : m * 16 + (lane & 15));
+        x_at[m] = min(t, int64_t(g.tokens) - 1) * g.ldx;
     }
     for (int pass = 0, a; (a = rows.next()) >= 0; ++pass) {
         if (pass % int(gridDim.z) != int(blockIdx.z)) continue;
@@ -255,33 +263,43 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterArgs g, A
             for (int m = 0; m < MR; ++m) acc[n][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         // raw loads of one step, in flight while the step before is multiplied
         struct Step {
-            u32x4 w[NR], x[MR][XT == kF32 ? 2 : 1];
+            u32x4 w[NR], x[kLoads];
         };
-        auto load = [&](Step &q, int k) {
-            const int kc = k < k1 ? k : 0;       // past the slice: some values, not used
+        auto load = [&](Step &q, int step) {
+            // past the slice: some values, not used
+            const int k = k0 + step * kAdapterStep, kc = k < k1 ? k : 0;
+            const int kv = kx + step * kAdapterStep, kvc = kv < k1 ? kv : 0;
 #pragma unroll
             for (int n = 0; n < NR; ++n) q.w[n] = *reinterpret_cast<const u32x4 *>(a_row[n] + kc);
+            using T = typename Elem<XT>::T;
 #pragma unroll
-            for (int m = 0; m < MR; ++m) {
-                using T = typename Elem<XT>::T;
-                const u32x4 *src = reinterpret_cast<const u32x4 *>(static_cast<const T *>(g.x) + x_at[m] + kc);
-                q.x[m][0] = src[0];
-                if constexpr (XT == kF32) q.x[m][1] = src[1];
-            }
+            for (int m = 0; m < kLoads; ++m)
+                q.x[m] = *reinterpret_cast<const u32x4 *>(static_cast<const T *>(g.x) + x_at[m] + kvc);
         };
-        auto multiply = [&](const Step &q, int k) {
-            const bool in = k < k1;
+        auto multiply = [&](const Step &q, int step) {
+            const bool in = k0 + step * kAdapterStep < k1;
             const u32x4 zero = {0, 0, 0, 0};
+            if constexpr (XT == kF32) {
+                const bool x_in = kx + step * kAdapterStep < k1;
+                __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                for (int m = 0; m < kLoads; ++m)
+                    *reinterpret_cast<u32x4 *>(&lds.x[wave][m * 8 + (lane >> 3)][(lane & 7) * 4]) =
+                        x_in ? q.x[m] : zero;
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+            }
             u32x4 v[MR][kXP];
 #pragma unroll
             for (int m = 0; m < MR; ++m) {
                 if constexpr (XT == kF32) {
                     float f[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) f[j] = in ? __uint_as_float(q.x[m][j / 4][j % 4]) : 0.0f;
+                    const float *src = &lds.x[wave][m * 16 + (lane & 15)][(lane >> 4) * 8];
+                    *reinterpret_cast<f32x4 *>(f) = *reinterpret_cast<const f32x4 *>(src);
+                    *reinterpret_cast<f32x4 *>(f + 4) = *reinterpret_cast<const f32x4 *>(src + 4);
                     split<3>(f, v[m]);
                 } else {
-                    v[m][0] = in ? q.x[m][0] : zero;
+                    v[m][0] = in ? q.x[m] : zero;
                 }
             }
 #pragma unroll
@@ -299,23 +317,24 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterArgs g, A
             }
         };
         Step one, two;
-        load(one, k0);
+        load(one, 0);
         const int steps = (k1 - (k0 - (lane >> 4) * 8) + kAdapterStep - 1) / kAdapterStep;
         for (int q = 0; q < steps; q += 2) {
-            const int k = k0 + q * kAdapterStep;
-            load(two, k + kAdapterStep);
-            multiply(one, k);
-            load(one, k + 2 * kAdapterStep);
-            multiply(two, k + kAdapterStep);
+            load(two, q + 1);
+            multiply(one, q);
+            load(one, q + 2);
+            multiply(two, q + 1);
         }
+        __syncthreads();            // the union: every wave is done with its values of x
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
-            for (int m = 0; m < MR; ++m) red[wave][n][m][lane] = acc[n][m];
+            for (int m = 0; m < MR; ++m) lds.red[wave][n][m][lane] = acc[n][m];
         __syncthreads();
         for (int c = threadIdx.x; c < NR * MR * 64; c += kThreads) {
             const int n = c / (MR * 64), m = c / 64 % MR, l = c & 63;
-            const f32x4 h = (red[0][n][m][l] + red[1][n][m][l]) + (red[2][n][m][l] + red[3][n][m][l]);
+            const f32x4 h = (lds.red[0][n][m][l] + lds.red[1][n][m][l]) +
+                            (lds.red[2][n][m][l] + lds.red[3][n][m][l]);
             const int row = m * 16 + (l & 15), r = r0 + n * 16 + (l >> 4) * 4;
             const int64_t t = first + row;
             if (r < g.rank && t < g.tokens && adapter_of(g, t) == a)
