@@ -249,13 +249,12 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterArgs g, A
     }
     for (int pass = 0, a; (a = rows.next()) >= 0; ++pass) {
         if (pass % int(gridDim.z) != int(blockIdx.z)) continue;
-        const int rank = rank_of(g, a);
-        if (r0 >= rank) continue;
+        if (r0 > 0 && r0 >= rank_of(g, a)) continue;
         const uint16_t *mat = static_cast<const uint16_t *>(g.a) + int64_t(a) * g.rank * g.n_in;
         const uint16_t *a_row[NR];
 #pragma unroll
         for (int n = 0; n < NR; ++n)
-            a_row[n] = mat + int64_t(min(r0 + n * 16 + (lane & 15), rank - 1)) * g.n_in;
+            a_row[n] = mat + int64_t(min(r0 + n * 16 + (lane & 15), g.rank - 1)) * g.n_in;
         f32x4 acc[NR][MR];
 #pragma unroll
         for (int n = 0; n < NR; ++n)
@@ -345,8 +344,10 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterArgs g, A
 }
 
 // The update of a tile of 16 * MR rows, 256 outputs at a time (64 per wave).
-// h, its planes added, stands in LDS; the matrix unit's rows are outputs, its
-// columns rows of the tile.  The 16 x 64 results pass through LDS so that base
+// h, its planes added, stands in LDS, all rows of the tile at once where the
+// rank fits (its loads then wait for nothing else); the matrix unit's rows are
+// outputs, its columns rows of the tile, and a pass's results are taken from
+// the columns whose rows have its adapter.  The 16 x 64 results pass through LDS so that base
 // and out move in whole row segments: 256 bytes of a row per 16 lanes reach
 // 6.2 TB/s in a copy of this shape, the 64 that the matrix unit's layout gives
 // 4.6.  KB: blocks of 32 rank values whose part of b is held in registers and
@@ -392,10 +393,36 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterArgs g, Ada
             for (int i = 0; i < kParts; ++i)
                 b_run[m][i] = stream_load<Run>(base + row[m][i] * g.ldb + min(n, g.n_out - kRun));
     };
+    auto stage = [&](int b) {
+        for (int c = threadIdx.x; c < 16 * MR * (kUpRank / 4); c += kThreads) {
+            const int r0 = c / (kUpRank / 4), r = b + c % (kUpRank / 4) * 4;
+            if (r >= g.rank) continue;
+            const float *src = g.ws + min(first + r0, int64_t(g.tokens) - 1) * g.rank + r;
+            const int64_t plane = int64_t(g.tokens) * g.rank;
+            f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int q = 0; q < s.splits; q += 4) {
+                f32x4 p[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    p[i] = *reinterpret_cast<const f32x4 *>(src + min(q + i, s.splits - 1) * plane);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (q + i < s.splits) v += p[i];
+            }
+            *reinterpret_cast<f32x4 *>(&h[r0][r - b]) = v;
+        }
+    };
+    load_base(n_begin + col);
+    if constexpr (KB > 0) {
+        stage(0);
+        __syncthreads();
+    }
     // rows without an adapter
-    if (blockIdx.z == 0 && g.out != g.base && __popcll(rows.left) < min(int64_t(16 * MR), g.tokens - first))
+    const bool copied = blockIdx.z == 0 && g.out != g.base &&
+                        __popcll(rows.left) < min(int64_t(16 * MR), g.tokens - first);
+    if (copied)
         for (int n = n_begin + col; n < n_end; n += kThreads) {
-            load_base(n);
+            if (n > n_begin + col) load_base(n);
 #pragma unroll
             for (int m = 0; m < MR; ++m)
 #pragma unroll
@@ -422,34 +449,7 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterArgs g, Ada
                     for (int j = 0; j < 4; ++j) w_run[q][j] = load_b(n0, j, q * 32);
         };
         load_weights(n_begin);
-        load_base(n_begin + col);
-        auto stage = [&](int b) {
-            __syncthreads();
-            for (int c = threadIdx.x; c < 16 * MR * (kUpRank / 4); c += kThreads) {
-                const int r0 = c / (kUpRank / 4), r = b + c % (kUpRank / 4) * 4;
-                const int64_t t = first + r0;
-                f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-                if (r < rank && t < g.tokens) {
-                    const float *src = g.ws + t * g.rank + r;
-                    const int64_t plane = int64_t(g.tokens) * g.rank;
-                    for (int q = 0; q < s.splits; q += 4) {
-                        f32x4 p[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            p[i] = *reinterpret_cast<const f32x4 *>(src + min(q + i, s.splits - 1) * plane);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (q + i < s.splits) v += p[i];
-                    }
-                }
-                // values past the rank, and rows of other adapters, may hold anything
-                const bool mine = t < g.tokens && adapter_of(g, t) == a;
-                for (int i = 0; i < 4; ++i) v[i] = mine && r + i < rank ? v[i] : 0.0f;
-                *reinterpret_cast<f32x4 *>(&h[r0][r - b]) = v;
-            }
-            __syncthreads();
-        };
-        if (rank <= kUpRank) stage(0);
+        if (pass > 0 || copied) load_base(n_begin + col);
         for (int n0 = n_begin; n0 < n_end; n0 += kThreads) {
             f32x4 acc[4][MR];
 #pragma unroll
@@ -464,6 +464,10 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterArgs g, Ada
                     const float *src = &h[m * 16 + (lane & 15)][k - b + (lane >> 4) * 8];
                     *reinterpret_cast<f32x4 *>(f) = *reinterpret_cast<const f32x4 *>(src);
                     *reinterpret_cast<f32x4 *>(f + 4) = *reinterpret_cast<const f32x4 *>(src + 4);
+                    // values past the rank may be anything, and 0 times that is not 0
+                    if (k + 32 > rank)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) f[i] = k + (lane >> 4) * 8 + i < rank ? f[i] : 0.0f;
                     split<kHP>(f, v[m]);
                 }
 #pragma unroll
@@ -490,7 +494,9 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterArgs g, Ada
                 if (n0 + kThreads < n_end) load_weights(n0 + kThreads);
             } else {
                 for (int b = 0; b < rank; b += kUpRank) {
-                    if (rank > kUpRank) stage(b);
+                    __syncthreads();
+                    stage(b);
+                    __syncthreads();
                     for (int k = b; k < min(rank, b + kUpRank); k += 32)
                         multiply(b, k, [&](int j) { return load_b(n0, j, k); });
                 }
