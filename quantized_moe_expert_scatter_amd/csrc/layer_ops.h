@@ -34,6 +34,18 @@ struct RouteArgs {
     int64_t ldd;
 };
 
+// The router holds a token's logits in one wave, J per lane.
+constexpr int route_lane_experts(int n_expert) {
+    int j = 1;
+    while (j * 64 < n_expert) j *= 2;
+    return j;
+}
+// Waves of a workgroup of the router with statistics: as many as its LDS (a
+// row of fp32 sums per wave) allows.
+constexpr int balance_waves(int lane_experts) {
+    return lane_experts <= 8 ? 16 : lane_experts == 16 ? 8 : 4;
+}
+
 // The balance statistics are summed in pieces: the tokens are cut into ranges
 // of range_tokens, one workgroup each, and a range's part of a sequence is a
 // piece.  Sequences are in token order, so (range, sequence) -> range +
@@ -44,17 +56,18 @@ struct BalanceLayout {
     size_t probs;      // fp32 [n_ranges + n_seq][E]: sums of p over a piece
     size_t counts;     // int32, the same shape
     size_t loss;       // fp32 [n_seq][column blocks]: parts of the loss
+    size_t done;       // int32: joining workgroups that have written theirs
     size_t total;
 };
 
-constexpr int kBalanceCols = 64;         // columns of one joining workgroup
-constexpr int kBalanceMaxRanges = 1024;  // four workgroups per CU
-constexpr int kBalanceMinRange = 4;      // one token per wave
+constexpr int kBalanceCols = 64;        // columns of one joining workgroup
+constexpr int kBalanceMaxRanges = 512;  // two workgroups per CU
 
 inline BalanceLayout balance_layout(int tokens, int n_expert, int n_seq) {
     BalanceLayout L{};
-    const int per = int(((long long)tokens + kBalanceMaxRanges - 1) / kBalanceMaxRanges);
-    L.range_tokens = per > kBalanceMinRange ? (per + 3) / 4 * 4 : kBalanceMinRange;
+    const int waves = balance_waves(route_lane_experts(n_expert));
+    const long long per = ((long long)tokens + kBalanceMaxRanges - 1) / kBalanceMaxRanges;
+    L.range_tokens = per > waves ? int((per + waves - 1) / waves * waves) : waves;
     L.n_ranges = int(((long long)tokens + L.range_tokens - 1) / L.range_tokens);
     const size_t cells = (size_t(L.n_ranges) + size_t(n_seq)) * size_t(n_expert);
     auto up = [](size_t x) { return (x + 15) & ~size_t(15); };
@@ -62,6 +75,7 @@ inline BalanceLayout balance_layout(int tokens, int n_expert, int n_seq) {
     L.probs = o;  o += up(cells * 4);
     L.counts = o; o += up(cells * 4);
     L.loss = o;   o += up(size_t(n_seq) * size_t((n_expert + kBalanceCols - 1) / kBalanceCols) * 4);
+    L.done = o;   o += 16;
     L.total = o;
     return L;
 }

@@ -54,36 +54,114 @@ __device__ __forceinline__ void load_row(const void *logits, int64_t at, int n_e
     }
 }
 
+// Sorts N keys, largest first (a network: the same steps whatever the keys).
+template <int N>
+__device__ __forceinline__ void sort_keys(uint32_t (&k)[N]) {
+    auto order = [&](int i, int j) {
+        const uint32_t hi = max(k[i], k[j]);
+        k[j] = min(k[i], k[j]);
+        k[i] = hi;
+    };
+    if constexpr (N == 2) order(0, 1);
+    if constexpr (N == 4) { order(0, 1); order(2, 3); order(0, 2); order(1, 3); order(1, 2); }
+    if constexpr (N == 8) {
+        order(0, 1); order(2, 3); order(4, 5); order(6, 7);
+        order(0, 2); order(1, 3); order(4, 6); order(5, 7);
+        order(1, 2); order(5, 6); order(0, 4); order(3, 7);
+        order(1, 5); order(2, 6);
+        order(1, 4); order(3, 6);
+        order(2, 4); order(3, 5);
+        order(3, 4);
+    }
+}
+
 // The topk largest: lane k < topk receives the k-th's expert and logit.
-// Returns the row's largest logit (NaN if the row holds one).
+// Returns the row's largest logit (NaN if the row holds one).  `spare` is the
+// wave's own LDS, 64 * J keys.
+//   Up to 8 experts a lane the lanes sort theirs first: a round then takes the
+// largest of the 64 heads (six cross-lane steps), and the lane that had it
+// moves its list up.  Which of its experts that was is found afterwards for all
+// rounds at once, from the keys in LDS: the expert is the (times+1)-th of the
+// lane's keys equal to the round's, `times` the rounds just before it with the
+// same lane and key (equal keys leave a lane one after the other).
 template <int J>
 __device__ __forceinline__ float choose(const float (&v)[J], int n_expert, int topk, int lane, int &id,
-                                        float &logit) {
+                                        float &logit, uint32_t *spare) {
     uint32_t key[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) key[j] = lane * J + j < n_expert ? order_key(v[j]) : 0u;
     uint32_t first = 0, mine = 0;
     id = 0;
-    for (int k = 0; k < topk; ++k) {
-        uint32_t best = key[0];
+    if constexpr (J <= 8) {
+        __builtin_amdgcn_wave_barrier();
+        if constexpr (J > 1)
 #pragma unroll
-        for (int j = 1; j < J; ++j) best = max(best, key[j]);
-        const uint32_t top = wave_max(best);
-        const int owner = __ffsll((unsigned long long)__ballot(best == top)) - 1;
-        int at = 0;
+            for (int j = 0; j < J; ++j) spare[lane * J + j] = key[j];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        sort_keys(key);
+        int from = 0, times = 0, my_from = 0, my_times = 0;
+        uint32_t before = 0;
+        for (int k = 0; k < topk; ++k) {
+            const uint32_t top = wave_max(key[0]);
+            const int owner = __ffsll((unsigned long long)__ballot(key[0] == top)) - 1;
+            times = owner == from && top == before ? times + 1 : 0;
+            from = owner;
+            before = top;
+            if (lane == owner) {
 #pragma unroll
-        for (int j = J - 1; j >= 0; --j) at = key[j] == top ? j : at;
-        const int expert = owner * J + __builtin_amdgcn_readlane(at, owner);
-#pragma unroll
-        for (int j = 0; j < J; ++j) key[j] = (lane * J + j == expert) ? 0u : key[j];
-        if (lane == k) {
-            id = expert;
-            mine = top;
+                for (int j = 0; j + 1 < J; ++j) key[j] = key[j + 1];
+                key[J - 1] = 0;
+            }
+            const bool here = lane == k;
+            mine = here ? top : mine;
+            my_from = here ? owner : my_from;
+            if constexpr (J > 1) my_times = here ? times : my_times;
+            first = k == 0 ? top : first;
         }
-        if (k == 0) first = top;
+        id = my_from * J;
+        if constexpr (J > 1) {
+            int at = 0, skip = my_times;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const bool hit = spare[my_from * J + j] == mine;
+                at = hit && skip == 0 ? j : at;
+                skip -= hit;
+            }
+            id += at;
+        }
+    } else {
+        for (int k = 0; k < topk; ++k) {
+            uint32_t best = key[0];
+#pragma unroll
+            for (int j = 1; j < J; ++j) best = max(best, key[j]);
+            const uint32_t top = wave_max(best);
+            const int owner = __ffsll((unsigned long long)__ballot(best == top)) - 1;
+            int at = 0;
+#pragma unroll
+            for (int j = J - 1; j >= 0; --j) at = key[j] == top ? j : at;
+            const int expert = owner * J + __builtin_amdgcn_readlane(at, owner);
+#pragma unroll
+            for (int j = 0; j < J; ++j) key[j] = (lane * J + j == expert) ? 0u : key[j];
+            if (lane == k) {
+                id = expert;
+                mine = top;
+            }
+            if (k == 0) first = top;
+        }
     }
     logit = key_value(mine);
     return key_value(first);
+}
+
+// e^x for x <= 0 (0 for -inf, NaN for NaN), within two steps of fp32 and with
+// subnormal results: x = (n + f) ln 2, the fraction taken with log2(e) in two
+// parts, so that its error does not grow with x.
+__device__ __forceinline__ float exp_neg(float x) {
+    constexpr float kHi = 1.44269502f, kLo = 1.92596303e-8f;      // log2(e) = kHi + kLo
+    const float n = __builtin_rintf(fmaxf(x * kHi, -300.0f));
+    const float f = __builtin_fmaf(x, kLo, __builtin_fmaf(x, kHi, -n));
+    return __builtin_ldexpf(__builtin_amdgcn_exp2f(f), int(n));
 }
 
 // What the exponents are taken against: the row's largest logit, 0 where every
@@ -108,21 +186,21 @@ __device__ __forceinline__ int sequence_of(const int32_t *seq_off, int n_seq, in
 // Routes token t; with STATS the row's softmax is added to acc.
 template <int J, int DT, bool VEC, bool STATS>
 __device__ __forceinline__ void route_token(const RouteArgs &a, int t, int lane, bool count,
-                                            float (&acc)[J], int *hist) {
+                                            float (&acc)[J], int *hist, uint32_t *spare) {
     float v[J];
     load_row<J, DT, VEC>(a.logits, int64_t(t) * a.ld, a.n_expert, lane, v);
     int id;
     float logit;
-    const float top = choose<J>(v, a.n_expert, a.topk, lane, id, logit);
+    const float top = choose<J>(v, a.n_expert, a.topk, lane, id, logit, spare);
     const float shift = softmax_shift(top);
     const bool chosen = lane < a.topk;
-    const float e = chosen ? expf(logit - shift) : 0.0f;
+    const float e = chosen ? exp_neg(logit - shift) : 0.0f;
     float inv = 0.0f;
     if (STATS || !a.renorm) {
         float part = 0.0f;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            v[j] = expf(v[j] - shift);
+            v[j] = exp_neg(v[j] - shift);
             part += v[j];
         }
         const float sum = wave_sum(part);
@@ -146,25 +224,28 @@ __device__ __forceinline__ void route_token(const RouteArgs &a, int t, int lane,
 template <int J, int DT, bool VEC>
 __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
     const int lane = threadIdx.x & 63;
+    __shared__ alignas(16) uint32_t spare[kRouteWaves][J <= 8 ? 64 * J : 1];
     float none[J];
     for (int64_t t = int64_t(blockIdx.x) * kRouteWaves + (threadIdx.x >> 6); t < a.tokens;
          t += int64_t(gridDim.x) * kRouteWaves)
-        route_token<J, DT, VEC, false>(a, int(t), lane, false, none, nullptr);
+        route_token<J, DT, VEC, false>(a, int(t), lane, false, none, nullptr, spare[threadIdx.x >> 6]);
 }
 
 // One workgroup per range of tokens: routes them and sums each sequence's part
-// of the range, p in registers (then over the four waves through LDS), the
-// choices in an LDS histogram.
+// of the range, p in registers (then over the waves through LDS), the choices
+// in an LDS histogram.
 template <int J, int DT, bool VEC>
-__global__ __launch_bounds__(kRouteThreads) void route_balance_kernel(RouteArgs a, BalanceLayout L) {
-    __shared__ float red[kRouteWaves][64 * J];
+__global__ __launch_bounds__(64 * balance_waves(J)) void route_balance_kernel(RouteArgs a, BalanceLayout L) {
+    constexpr int kWaves = balance_waves(J), kThreads = 64 * kWaves;
+    __shared__ alignas(16) float red[kWaves][64 * J];       // the waves' sums; while routing, their keys
     __shared__ int hist[64 * J];
+    if (blockIdx.x == 0 && threadIdx.x == 0) *reinterpret_cast<int32_t *>(a.ws + L.done) = 0;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     float *out_p = reinterpret_cast<float *>(a.ws + L.probs);
     int32_t *out_c = reinterpret_cast<int32_t *>(a.ws + L.counts);
     const int t0 = int(blockIdx.x) * L.range_tokens;
     const int t1 = a.tokens - t0 < L.range_tokens ? a.tokens : t0 + L.range_tokens;
-    for (int e = threadIdx.x; e < 64 * J; e += kRouteThreads) hist[e] = 0;
+    for (int e = threadIdx.x; e < 64 * J; e += kThreads) hist[e] = 0;
     __syncthreads();
     float acc[J];
 #pragma unroll
@@ -182,8 +263,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_balance_kernel(RouteArgs 
                 end = min(e, t1);
             }
         }
-        for (int t = pos + wave; t < end; t += kRouteWaves)
-            route_token<J, DT, VEC, true>(a, t, lane, inside, acc, hist);
+        for (int t = pos + wave; t < end; t += kWaves)
+            route_token<J, DT, VEC, true>(a, t, lane, inside, acc, hist, reinterpret_cast<uint32_t *>(red[wave]));
         if (inside) {
 #pragma unroll
             for (int j = 0; j < J; ++j) {
@@ -192,8 +273,11 @@ __global__ __launch_bounds__(kRouteThreads) void route_balance_kernel(RouteArgs 
             }
             __syncthreads();
             const size_t at = (size_t(blockIdx.x) + s) * a.n_expert;
-            for (int e = threadIdx.x; e < a.n_expert; e += kRouteThreads) {
-                out_p[at + e] = (red[0][e] + red[1][e]) + (red[2][e] + red[3][e]);
+            for (int e = threadIdx.x; e < a.n_expert; e += kThreads) {
+                float p = red[0][e];
+#pragma unroll
+                for (int w = 1; w < kWaves; ++w) p += red[w][e];
+                out_p[at + e] = p;
                 out_c[at + e] = hist[e];
                 hist[e] = 0;
             }
@@ -204,13 +288,16 @@ __global__ __launch_bounds__(kRouteThreads) void route_balance_kernel(RouteArgs 
 }
 
 // Joins a sequence's pieces for 64 experts: a wave takes every 16th piece, the
-// waves are added in order.  Long sums in 64 bits.
+// waves are added in order, long sums in 64 bits.  The workgroup that is last
+// to write its parts of the loss adds them all, in their order.
 __global__ __launch_bounds__(64 * kJoinWaves) void balance_join_kernel(RouteArgs a, BalanceLayout L,
                                                                        int cols) {
     __shared__ double red_p[kJoinWaves][kBalanceCols];
     __shared__ int red_c[kJoinWaves][kBalanceCols];
+    __shared__ bool last_group;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t jobs = int64_t(a.n_seq) * cols;
+    float *loss = reinterpret_cast<float *>(a.ws + L.loss);
     for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
         const int s = int(job / cols), e = int(job % cols) * kBalanceCols + lane;
         const int b = min(max(a.seq_off[s], 0), a.tokens);
@@ -218,19 +305,20 @@ __global__ __launch_bounds__(64 * kJoinWaves) void balance_join_kernel(RouteArgs
         double p = 0.0;
         int c = 0;
         if (n > 0 && e < a.n_expert) {
-            const float *in_p = reinterpret_cast<const float *>(a.ws + L.probs);
-            const int32_t *in_c = reinterpret_cast<const int32_t *>(a.ws + L.counts);
+            const float *in_p = reinterpret_cast<const float *>(a.ws + L.probs) + size_t(s) * a.n_expert + e;
+            const int32_t *in_c = reinterpret_cast<const int32_t *>(a.ws + L.counts) + size_t(s) * a.n_expert + e;
             const int last = (b + n - 1) / L.range_tokens;
+#pragma unroll 8
             for (int r = b / L.range_tokens + wave; r <= last; r += kJoinWaves) {
-                const size_t at = (size_t(r) + s) * a.n_expert + e;
-                p += double(in_p[at]);
-                c += in_c[at];
+                p += double(in_p[size_t(r) * a.n_expert]);
+                c += in_c[size_t(r) * a.n_expert];
             }
         }
         red_p[wave][lane] = p;
         red_c[wave][lane] = c;
         __syncthreads();
         if (wave == 0) {
+#pragma unroll
             for (int i = 1; i < kJoinWaves; ++i) {
                 p += red_p[i][lane];
                 c += red_c[i][lane];
@@ -242,25 +330,29 @@ __global__ __launch_bounds__(64 * kJoinWaves) void balance_join_kernel(RouteArgs
             }
             const float part = wave_sum(float(c) * mean);
             if (lane == 0)
-                reinterpret_cast<float *>(a.ws + L.loss)[job] =
-                    n > 0 ? part * (float(a.n_expert) / (float(a.topk) * float(n))) : 0.0f;
+                __hip_atomic_store(loss + job,
+                                   n > 0 ? part * (float(a.n_expert) / (float(a.topk) * float(n))) : 0.0f,
+                                   __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
         __syncthreads();
     }
-}
-
-__global__ __launch_bounds__(1024) void balance_loss_kernel(RouteArgs a, BalanceLayout L, int64_t parts) {
-    __shared__ double red[1024];
-    const float *in = reinterpret_cast<const float *>(a.ws + L.loss);
-    double sum = 0.0;
-    for (int64_t i = threadIdx.x; i < parts; i += 1024) sum += double(in[i]);
-    red[threadIdx.x] = sum;
+    if (threadIdx.x == 0)
+        last_group = gridDim.x == 1 ||
+                     __hip_atomic_fetch_add(reinterpret_cast<int32_t *>(a.ws + L.done), 1, __ATOMIC_ACQ_REL,
+                                            __HIP_MEMORY_SCOPE_AGENT) == int(gridDim.x) - 1;
     __syncthreads();
-    for (int half = 512; half > 0; half >>= 1) {
-        if (int(threadIdx.x) < half) red[threadIdx.x] += red[threadIdx.x + half];
+    if (!last_group) return;
+    double *sums = &red_p[0][0];
+    double sum = 0.0;
+    for (int64_t i = threadIdx.x; i < jobs; i += 64 * kJoinWaves)
+        sum += double(__hip_atomic_load(loss + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+    sums[threadIdx.x] = sum;
+    __syncthreads();
+    for (int half = 32 * kJoinWaves; half > 0; half >>= 1) {
+        if (int(threadIdx.x) < half) sums[threadIdx.x] += sums[threadIdx.x + half];
         __syncthreads();
     }
-    if (threadIdx.x == 0) a.loss[0] = float(double(a.coef) / a.n_seq * red[0]);
+    if (threadIdx.x == 0) a.loss[0] = float(double(a.coef) / a.n_seq * sums[0]);
 }
 
 // The gradient of one token's row.
@@ -308,14 +400,14 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteArgs
         float part = 0.0f, pc = 0.0f;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            v[j] = expf(v[j] - shift);
+            v[j] = exp_neg(v[j] - shift);
             part += v[j];
             pc = __builtin_fmaf(v[j], c[j], pc);
         }
         const float sum = wave_sum(part);
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         float z = wave_sum(pc) * inv;
-        float e = id >= 0 ? expf(logit - shift) : 0.0f;
+        float e = id >= 0 ? exp_neg(logit - shift) : 0.0f;
         float add;
         if (a.renorm) {
             const float chosen = wave_sum(e);
@@ -348,13 +440,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteArgs
     }
 }
 
-// Lanes hold J experts each; wide loads need whole runs of J at a multiple of
-// their size, at every row.
-int experts_per_lane(int n_expert) {
-    int j = 1;
-    while (j * 64 < n_expert) j *= 2;
-    return j;
-}
+// Wide loads need whole runs of J experts at a multiple of their size, at
+// every row.
 bool wide_rows(int j, int n_expert, int64_t ld, int dtype) {
     const int size = dtype == kF32 ? 4 : 2;
     const int run = j * size < 16 ? j * size : 16;
@@ -390,7 +477,7 @@ dim3 token_grid(int tokens) {
 }  // namespace
 
 hipError_t launch_route(const RouteArgs &a, hipStream_t stream) {
-    const int j = experts_per_lane(a.n_expert);
+    const int j = route_lane_experts(a.n_expert);
     return by_shape(j, a.dtype, wide_rows(j, a.n_expert, a.ld, a.dtype), [&](auto J, auto DT, auto V) {
         hipLaunchKernelGGL((route_kernel<J.value, DT.value, V.value>), token_grid(a.tokens),
                            dim3(kRouteThreads), 0, stream, a);
@@ -400,27 +487,25 @@ hipError_t launch_route(const RouteArgs &a, hipStream_t stream) {
 
 hipError_t launch_route_balance(const RouteArgs &a, hipStream_t stream) {
     const BalanceLayout L = balance_layout(a.tokens, a.n_expert, a.n_seq);
-    const int j = experts_per_lane(a.n_expert);
+    const int j = route_lane_experts(a.n_expert);
     hipError_t err = hipSuccess;
     if (a.tokens > 0)
         err = by_shape(j, a.dtype, wide_rows(j, a.n_expert, a.ld, a.dtype), [&](auto J, auto DT, auto V) {
             hipLaunchKernelGGL((route_balance_kernel<J.value, DT.value, V.value>), dim3(L.n_ranges),
-                               dim3(kRouteThreads), 0, stream, a, L);
+                               dim3(64 * balance_waves(J.value)), 0, stream, a, L);
             return hipGetLastError();
         });
     if (err != hipSuccess) return err;
     const int cols = (a.n_expert + kBalanceCols - 1) / kBalanceCols;
     const int64_t jobs = int64_t(cols) * a.n_seq;
-    hipLaunchKernelGGL(balance_join_kernel, dim3(unsigned(jobs < kJoinMaxGroups ? jobs : kJoinMaxGroups)),
-                       dim3(64 * kJoinWaves), 0, stream, a, L, cols);
-    err = hipGetLastError();
-    if (err != hipSuccess) return err;
-    hipLaunchKernelGGL(balance_loss_kernel, dim3(1), dim3(1024), 0, stream, a, L, jobs);
+    // without tokens nothing has cleared the count of finished workgroups: one does it all
+    const int64_t groups = a.tokens == 0 ? 1 : jobs < kJoinMaxGroups ? jobs : kJoinMaxGroups;
+    hipLaunchKernelGGL(balance_join_kernel, dim3(unsigned(groups)), dim3(64 * kJoinWaves), 0, stream, a, L, cols);
     return hipGetLastError();
 }
 
 hipError_t launch_route_backward(const RouteArgs &a, hipStream_t stream) {
-    const int j = experts_per_lane(a.n_expert);
+    const int j = route_lane_experts(a.n_expert);
     const bool vec = wide_rows(j, a.n_expert, a.ld, a.dtype) && wide_rows(j, a.n_expert, a.ldd, a.dtype);
     return by_shape(j, a.dtype, vec, [&](auto J, auto DT, auto V) {
         hipLaunchKernelGGL((route_backward_kernel<J.value, DT.value, V.value>), token_grid(a.tokens),

@@ -149,8 +149,10 @@ def test_balance(T, E, K, bounds, dtype, kind):
     else:
         want_c, want_p, want_l = np.zeros((S, E)), np.zeros((S, E)), 0.0
     assert np.array_equal(counts[:S].cpu().numpy(), want_c)
-    # a wave adds its share of a range of at most max(4, T/1024 + 3) tokens, then four waves
-    chain = max(4, T // 1024 + 4) / 4 + 2
+    # the longest chain of additions in fp32: a range holds at most max(16, T/512 rounded up to a
+    # multiple of 16) tokens, dealt to at least 4 waves, then at most 16 waves are added (the
+    # ranges are added in 64 bits)
+    chain = max(16, (T // 512 // 16 + 1) * 16) / 4 + 16
     got = probs[:S].cpu().numpy()
     tol = want_p * (rtol(E) + (chain + 2) * ref.U) + 0.5 * ref.U
     assert np.all(np.abs(got - want_p) <= tol)
