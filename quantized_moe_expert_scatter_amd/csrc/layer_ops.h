@@ -60,7 +60,7 @@ struct BalanceLayout {
     size_t total;
 };
 
-constexpr int kBalanceCols = 64;        // columns of one joining workgroup
+constexpr int kBalanceCols = 16;        // columns of one joining workgroup
 constexpr int kBalanceMaxRanges = 512;  // two workgroups per CU
 
 inline BalanceLayout balance_layout(int tokens, int n_expert, int n_seq) {

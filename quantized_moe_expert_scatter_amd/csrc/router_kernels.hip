@@ -29,12 +29,12 @@ constexpr int kJoinMaxGroups = 4096;        // workgroups of the joining kernel;
 // No logit's key is 0 (that of -inf is 0x007fffff): 0 marks a place that
 // holds no expert, or one already taken.
 __device__ __forceinline__ uint32_t order_key(float f) {
-    if (f != f) return 0xffffffffu;
     const uint32_t u = __float_as_uint(f + 0.0f);
-    return (u >> 31) ? ~u : (u | 0x80000000u);
+    const uint32_t key = u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
+    return f == f ? key : 0xffffffffu;
 }
 __device__ __forceinline__ float key_value(uint32_t k) {
-    return __uint_as_float((k >> 31) ? (k & 0x7fffffffu) | ((k == 0xffffffffu) ? 0x7fffffffu : 0u) : ~k);
+    return __uint_as_float(k == 0xffffffffu ? 0x7fffffffu : k ^ (k >> 31 ? 0x80000000u : 0xffffffffu));
 }
 
 template <int J, int DT, bool VEC>
@@ -54,105 +54,116 @@ __device__ __forceinline__ void load_row(const void *logits, int64_t at, int n_e
     }
 }
 
-// Sorts N keys, largest first (a network: the same steps whatever the keys).
-template <int N>
-__device__ __forceinline__ void sort_keys(uint32_t (&k)[N]) {
-    auto order = [&](int i, int j) {
-        const uint32_t hi = max(k[i], k[j]);
-        k[j] = min(k[i], k[j]);
-        k[i] = hi;
-    };
-    if constexpr (N == 2) order(0, 1);
-    if constexpr (N == 4) { order(0, 1); order(2, 3); order(0, 2); order(1, 3); order(1, 2); }
-    if constexpr (N == 8) {
-        order(0, 1); order(2, 3); order(4, 5); order(6, 7);
-        order(0, 2); order(1, 3); order(4, 6); order(5, 7);
-        order(1, 2); order(5, 6); order(0, 4); order(3, 7);
-        order(1, 5); order(2, 6);
-        order(1, 4); order(3, 6);
-        order(2, 4); order(3, 5);
-        order(3, 4);
+// c[j] = f * the count of the lane's j-th expert (whole runs: the table's rows
+// are as the logits' then, 4 * J bytes apart and so aligned).
+template <int J, bool VEC>
+__device__ __forceinline__ void load_counts(const int32_t *row, int n_expert, int lane, float f, float (&c)[J]) {
+    struct alignas(J * 4 < 16 ? J * 4 : 16) Run { int32_t e[J]; };
+    if constexpr (VEC) {
+        if (lane * J < n_expert) {
+            const Run r = *reinterpret_cast<const Run *>(row + lane * J);
+#pragma unroll
+            for (int j = 0; j < J; ++j) c[j] = f * float(r.e[j]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            if (lane * J + j < n_expert) c[j] = f * float(row[lane * J + j]);
     }
 }
 
+// Sorts N = 2^n keys, largest first: Batcher's odd-even merging network, the
+// same steps whatever the keys (19 exchanges for 8, 191 for 32).
+template <int N>
+__device__ __forceinline__ void sort_keys(uint32_t (&k)[N]) {
+#pragma unroll
+    for (int p = 1; p < N; p *= 2)
+#pragma unroll
+        for (int d = p; d >= 1; d /= 2)
+#pragma unroll
+            for (int i = 0; i < N - d; ++i)
+                if (i >= d % p && (i - d % p) % (2 * d) < d && i / (2 * p) == (i + d) / (2 * p)) {
+                    const uint32_t hi = max(k[i], k[i + d]);
+                    k[i + d] = min(k[i], k[i + d]);
+                    k[i] = hi;
+                }
+}
+
 // The topk largest: lane k < topk receives the k-th's expert and logit.
-// Returns the row's largest logit (NaN if the row holds one).  `spare` is the
-// wave's own LDS, 64 * J keys.
-//   Up to 8 experts a lane the lanes sort theirs first: a round then takes the
-// largest of the 64 heads (six cross-lane steps), and the lane that had it
-// moves its list up.  Which of its experts that was is found afterwards for all
-// rounds at once, from the keys in LDS: the expert is the (times+1)-th of the
-// lane's keys equal to the round's, `times` the rounds just before it with the
-// same lane and key (equal keys leave a lane one after the other).
-template <int J>
-__device__ __forceinline__ float choose(const float (&v)[J], int n_expert, int topk, int lane, int &id,
-                                        float &logit, uint32_t *spare) {
+// Returns the row's largest logit (NaN if the row holds one).
+//   Each lane sorts its keys and puts the list into the wave's LDS (`lists`, 64
+// * (J + 1) keys, place by place, a 0 at its end); it keeps the head and the one behind it. A round
+// takes the largest head (six cross-lane steps) and its lane moves up: 13
+// vector operations a round, against 45 with the lists in registers and the
+// place searched for each time.  Which of the lane's experts it was is found
+// afterwards for all rounds at once, in the row itself: the (times+1)-th that
+// equals the round's logit, `times` being how many of the rounds just before
+// had the same lane and key (equal keys leave a lane one after the other, as
+// the first lane that has the largest key is always the one taken).
+template <int J, int DT, bool VEC>
+__device__ __forceinline__ float choose(const RouteArgs &a, int64_t row, const float (&v)[J], int lane, int &id,
+                                        float &logit, uint32_t *lists) {
     uint32_t key[J];
 #pragma unroll
-    for (int j = 0; j < J; ++j) key[j] = lane * J + j < n_expert ? order_key(v[j]) : 0u;
-    uint32_t first = 0, mine = 0;
-    id = 0;
-    if constexpr (J <= 8) {
+    for (int j = 0; j < J; ++j) {
+        const uint32_t k = order_key(v[j]);
+        key[j] = lane * J + (VEC ? 0 : j) < a.n_expert ? k : 0u;
+    }
+    sort_keys(key);
+    uint32_t head = key[0], next = 0;
+    if constexpr (J > 1) {
+        next = key[1];
         __builtin_amdgcn_wave_barrier();
-        if constexpr (J > 1)
 #pragma unroll
-            for (int j = 0; j < J; ++j) spare[lane * J + j] = key[j];
+        for (int j = 1; j <= J; ++j) lists[j * 64 + lane] = j < J ? key[j] : 0u;
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
-        sort_keys(key);
-        int from = 0, times = 0, my_from = 0, my_times = 0;
-        uint32_t before = 0;
-        for (int k = 0; k < topk; ++k) {
-            const uint32_t top = wave_max(key[0]);
-            const int owner = __ffsll((unsigned long long)__ballot(key[0] == top)) - 1;
-            times = owner == from && top == before ? times + 1 : 0;
-            from = owner;
-            before = top;
-            if (lane == owner) {
-#pragma unroll
-                for (int j = 0; j + 1 < J; ++j) key[j] = key[j + 1];
-                key[J - 1] = 0;
-            }
-            const bool here = lane == k;
-            mine = here ? top : mine;
-            my_from = here ? owner : my_from;
-            if constexpr (J > 1) my_times = here ? times : my_times;
-            first = k == 0 ? top : first;
-        }
-        id = my_from * J;
+    }
+    int at = 1;                          // the place of `next`
+    uint32_t first = 0;
+    int mine = 0, from = 0;
+    for (int k = 0; k < a.topk; ++k) {
+        const uint32_t top = wave_max(head);
+        const int owner = __builtin_ctzll(__ballot(head == top));
+        mine = lane == k ? int(top) : mine;
+        from = lane == k ? owner : from;
+        first = k == 0 ? top : first;
+        // J rounds at most take from one lane, the last of them finds the 0 at place J
+        const bool taken = lane == owner;
+        head = taken ? next : head;
         if constexpr (J > 1) {
-            int at = 0, skip = my_times;
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const bool hit = spare[my_from * J + j] == mine;
-                at = hit && skip == 0 ? j : at;
-                skip -= hit;
-            }
-            id += at;
-        }
-    } else {
-        for (int k = 0; k < topk; ++k) {
-            uint32_t best = key[0];
-#pragma unroll
-            for (int j = 1; j < J; ++j) best = max(best, key[j]);
-            const uint32_t top = wave_max(best);
-            const int owner = __ffsll((unsigned long long)__ballot(best == top)) - 1;
-            int at = 0;
-#pragma unroll
-            for (int j = J - 1; j >= 0; --j) at = key[j] == top ? j : at;
-            const int expert = owner * J + __builtin_amdgcn_readlane(at, owner);
-#pragma unroll
-            for (int j = 0; j < J; ++j) key[j] = (lane * J + j == expert) ? 0u : key[j];
-            if (lane == k) {
-                id = expert;
-                mine = top;
-            }
-            if (k == 0) first = top;
+            at += taken;
+            next = lists[min(at, J) * 64 + lane];
         }
     }
-    logit = key_value(mine);
+    id = from * J;
+    logit = key_value(uint32_t(mine));
+    if constexpr (J > 1) {
+        int times = 0;
+        bool same = lane < a.topk;
+        for (int d = 1; d < a.topk; ++d) {
+            const int m = __shfl_up(mine, d), f = __shfl_up(from, d);
+            same = same && lane >= d && m == mine && f == from;
+            if (!__any(same)) break;
+            times += same;
+        }
+        float u[J];
+        load_row<J, DT, VEC>(a.logits, row, a.n_expert, from, u);
+        int place = 0;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const bool hit = (u[j] == logit || (u[j] != u[j] && logit != logit)) && (VEC || from * J + j < a.n_expert);
+            place = hit && times == 0 ? j : place;
+            times -= hit;
+        }
+        id += place;
+    }
     return key_value(first);
 }
+
+// What the exponents are taken against: the row's largest logit, 0 where every
+// expert is closed (all exponentials are then 0).
+__device__ __forceinline__ float softmax_shift(float top) { return top == -INFINITY ? 0.0f : top; }
 
 // e^x for x <= 0 (0 for -inf, NaN for NaN), within two steps of fp32 and with
 // subnormal results: x = (n + f) ln 2, the fraction taken with log2(e) in two
@@ -163,10 +174,6 @@ __device__ __forceinline__ float exp_neg(float x) {
     const float f = __builtin_fmaf(x, kLo, __builtin_fmaf(x, kHi, -n));
     return __builtin_ldexpf(__builtin_amdgcn_exp2f(f), int(n));
 }
-
-// What the exponents are taken against: the row's largest logit, 0 where every
-// expert is closed (all exponentials are then 0).
-__device__ __forceinline__ float softmax_shift(float top) { return top == -INFINITY ? 0.0f : top; }
 
 // First sequence with seq_off[s+1] > t (n_seq if none), by 64 probes a step.
 __device__ __forceinline__ int sequence_of(const int32_t *seq_off, int n_seq, int t, int lane) {
@@ -186,12 +193,12 @@ __device__ __forceinline__ int sequence_of(const int32_t *seq_off, int n_seq, in
 // Routes token t; with STATS the row's softmax is added to acc.
 template <int J, int DT, bool VEC, bool STATS>
 __device__ __forceinline__ void route_token(const RouteArgs &a, int t, int lane, bool count,
-                                            float (&acc)[J], int *hist, uint32_t *spare) {
+                                            float (&acc)[J], int *hist, uint32_t *lists) {
     float v[J];
     load_row<J, DT, VEC>(a.logits, int64_t(t) * a.ld, a.n_expert, lane, v);
     int id;
     float logit;
-    const float top = choose<J>(v, a.n_expert, a.topk, lane, id, logit, spare);
+    const float top = choose<J, DT, VEC>(a, int64_t(t) * a.ld, v, lane, id, logit, lists);
     const float shift = softmax_shift(top);
     const bool chosen = lane < a.topk;
     const float e = chosen ? exp_neg(logit - shift) : 0.0f;
@@ -224,11 +231,11 @@ __device__ __forceinline__ void route_token(const RouteArgs &a, int t, int lane,
 template <int J, int DT, bool VEC>
 __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
     const int lane = threadIdx.x & 63;
-    __shared__ alignas(16) uint32_t spare[kRouteWaves][J <= 8 ? 64 * J : 1];
+    __shared__ alignas(16) uint32_t lists[kRouteWaves][64 * (J + 1)];
     float none[J];
     for (int64_t t = int64_t(blockIdx.x) * kRouteWaves + (threadIdx.x >> 6); t < a.tokens;
          t += int64_t(gridDim.x) * kRouteWaves)
-        route_token<J, DT, VEC, false>(a, int(t), lane, false, none, nullptr, spare[threadIdx.x >> 6]);
+        route_token<J, DT, VEC, false>(a, int(t), lane, false, none, nullptr, lists[threadIdx.x >> 6]);
 }
 
 // One workgroup per range of tokens: routes them and sums each sequence's part
@@ -237,7 +244,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
 template <int J, int DT, bool VEC>
 __global__ __launch_bounds__(64 * balance_waves(J)) void route_balance_kernel(RouteArgs a, BalanceLayout L) {
     constexpr int kWaves = balance_waves(J), kThreads = 64 * kWaves;
-    __shared__ alignas(16) float red[kWaves][64 * J];       // the waves' sums; while routing, their keys
+    __shared__ uint32_t red[kWaves][64 * (J + 1)];      // the waves' sums; while routing, their lists
     __shared__ int hist[64 * J];
     if (blockIdx.x == 0 && threadIdx.x == 0) *reinterpret_cast<int32_t *>(a.ws + L.done) = 0;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -264,19 +271,19 @@ __global__ __launch_bounds__(64 * balance_waves(J)) void route_balance_kernel(Ro
             }
         }
         for (int t = pos + wave; t < end; t += kWaves)
-            route_token<J, DT, VEC, true>(a, t, lane, inside, acc, hist, reinterpret_cast<uint32_t *>(red[wave]));
+            route_token<J, DT, VEC, true>(a, t, lane, inside, acc, hist, red[wave]);
         if (inside) {
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-                red[wave][lane * J + j] = acc[j];
+                red[wave][lane * J + j] = __float_as_uint(acc[j]);
                 acc[j] = 0.0f;
             }
             __syncthreads();
             const size_t at = (size_t(blockIdx.x) + s) * a.n_expert;
             for (int e = threadIdx.x; e < a.n_expert; e += kThreads) {
-                float p = red[0][e];
+                float p = __uint_as_float(red[0][e]);
 #pragma unroll
-                for (int w = 1; w < kWaves; ++w) p += red[w][e];
+                for (int w = 1; w < kWaves; ++w) p += __uint_as_float(red[w][e]);
                 out_p[at + e] = p;
                 out_c[at + e] = hist[e];
                 hist[e] = 0;
@@ -287,19 +294,22 @@ __global__ __launch_bounds__(64 * balance_waves(J)) void route_balance_kernel(Ro
     }
 }
 
-// Joins a sequence's pieces for 64 experts: a wave takes every 16th piece, the
-// waves are added in order, long sums in 64 bits.  The workgroup that is last
-// to write its parts of the loss adds them all, in their order.
+// Joins a sequence's pieces for 16 experts: a quarter wave takes every 64th
+// piece (8 of 512, all in flight at once), long sums in 64 bits and a fixed
+// order.  The workgroup that is last to write its parts of the loss adds them
+// all, in their order.
 __global__ __launch_bounds__(64 * kJoinWaves) void balance_join_kernel(RouteArgs a, BalanceLayout L,
                                                                        int cols) {
-    __shared__ double red_p[kJoinWaves][kBalanceCols];
-    __shared__ int red_c[kJoinWaves][kBalanceCols];
+    constexpr int kParts = 64 / kBalanceCols;        // pieces of a wave's access
+    __shared__ double red_p[kJoinWaves * 64];
+    __shared__ int red_c[kJoinWaves * 64];
     __shared__ bool last_group;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int col = lane % kBalanceCols;
     const int64_t jobs = int64_t(a.n_seq) * cols;
     float *loss = reinterpret_cast<float *>(a.ws + L.loss);
     for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
-        const int s = int(job / cols), e = int(job % cols) * kBalanceCols + lane;
+        const int s = int(job / cols), e = int(job % cols) * kBalanceCols + col;
         const int b = min(max(a.seq_off[s], 0), a.tokens);
         const int n = min(max(a.seq_off[s + 1], b), a.tokens) - b;
         double p = 0.0;
@@ -309,26 +319,36 @@ __global__ __launch_bounds__(64 * kJoinWaves) void balance_join_kernel(RouteArgs
             const int32_t *in_c = reinterpret_cast<const int32_t *>(a.ws + L.counts) + size_t(s) * a.n_expert + e;
             const int last = (b + n - 1) / L.range_tokens;
 #pragma unroll 8
-            for (int r = b / L.range_tokens + wave; r <= last; r += kJoinWaves) {
+            for (int r = b / L.range_tokens + wave * kParts + lane / kBalanceCols; r <= last;
+                 r += kJoinWaves * kParts) {
                 p += double(in_p[size_t(r) * a.n_expert]);
                 c += in_c[size_t(r) * a.n_expert];
             }
         }
-        red_p[wave][lane] = p;
-        red_c[wave][lane] = c;
+        red_p[threadIdx.x] = p;
+        red_c[threadIdx.x] = c;
         __syncthreads();
         if (wave == 0) {
+            // lane l adds rows l / 16, l / 16 + 4, ..., then the four are added
+            p = 0.0;
+            c = 0;
 #pragma unroll
-            for (int i = 1; i < kJoinWaves; ++i) {
-                p += red_p[i][lane];
-                c += red_c[i][lane];
+            for (int i = 0; i < kJoinWaves; ++i) {
+                p += red_p[i * 64 + lane];
+                c += red_c[i * 64 + lane];
+            }
+#pragma unroll
+            for (int d = kBalanceCols; d < 64; d *= 2) {
+                p += __shfl_xor(p, d);
+                c += __shfl_xor(c, d);
             }
             const float mean = n > 0 ? float(p / n) : 0.0f;
-            if (e < a.n_expert) {
+            const bool own = lane < kBalanceCols && e < a.n_expert;
+            if (own) {
                 a.counts[size_t(s) * a.n_expert + e] = c;
                 a.probs[size_t(s) * a.n_expert + e] = mean;
             }
-            const float part = wave_sum(float(c) * mean);
+            const float part = wave_sum(own ? float(c) * mean : 0.0f);
             if (lane == 0)
                 __hip_atomic_store(loss + job,
                                    n > 0 ? part * (float(a.n_expert) / (float(a.topk) * float(n))) : 0.0f,
@@ -342,7 +362,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void balance_join_kernel(RouteArgs
                                             __HIP_MEMORY_SCOPE_AGENT) == int(gridDim.x) - 1;
     __syncthreads();
     if (!last_group) return;
-    double *sums = &red_p[0][0];
+    double *sums = red_p;
     double sum = 0.0;
     for (int64_t i = threadIdx.x; i < jobs; i += 64 * kJoinWaves)
         sum += double(__hip_atomic_load(loss + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
@@ -355,11 +375,16 @@ __global__ __launch_bounds__(64 * kJoinWaves) void balance_join_kernel(RouteArgs
     if (threadIdx.x == 0) a.loss[0] = float(double(a.coef) / a.n_seq * sums[0]);
 }
 
-// The gradient of one token's row.
+// The gradient of one token's row.  The chosen experts' parts are scattered
+// through the wave's LDS: each chosen id first writes its lane's number and
+// reads it back, and only if an id is named twice (never by moe_route) are the
+// parts added one after the other.
 template <int J, int DT, bool VEC>
 __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteArgs a) {
     using T = typename Elem<DT>::T;
+    __shared__ alignas(16) float parts[kRouteWaves][64 * J];
     const int lane = threadIdx.x & 63;
+    float *part_of = parts[threadIdx.x >> 6];
     const float dloss = a.seq_off && a.dloss ? a.dloss[0] : 1.0f;
     for (int64_t t = int64_t(blockIdx.x) * kRouteWaves + (threadIdx.x >> 6); t < a.tokens;
          t += int64_t(gridDim.x) * kRouteWaves) {
@@ -370,11 +395,10 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteArgs
         float g = 0.0f, logit = -INFINITY;
         if (lane < a.topk) {
             id = a.ids[t * a.topk + lane];
-            if (id < 0 || id >= a.n_expert) id = -1;
-            if (id >= 0) {
-                logit = to_float<DT>(static_cast<const T *>(a.logits)[t * a.ld + id]);
-                if (a.dw) g = a.scale * a.dw[t * a.topk + lane];
-            }
+            if (a.dw) g = a.scale * a.dw[t * a.topk + lane];
+            id = id >= 0 && id < a.n_expert ? id : -1;
+            if (id >= 0) logit = to_float<DT>(static_cast<const T *>(a.logits)[t * a.ld + id]);
+            g = id >= 0 ? g : 0.0f;
         }
         // the loss's part
         float c[J];
@@ -386,17 +410,24 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteArgs
                 const float n = float(a.seq_off[s + 1] - a.seq_off[s]);
                 const float f = dloss * a.coef * float(a.n_expert) /
                                 (float(a.n_seq) * float(a.topk) * n * n);
-                const int32_t *counts = a.counts + size_t(s) * a.n_expert + lane * J;
-#pragma unroll
-                for (int j = 0; j < J; ++j)
-                    if (lane * J + j < a.n_expert) c[j] = f * float(counts[j]);
+                load_counts<J, VEC>(a.counts + size_t(s) * a.n_expert, a.n_expert, lane, f, c);
             }
         }
-        uint32_t best = 0;
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int j = 0; j < J; ++j)
-            best = max(best, lane * J + j < a.n_expert ? order_key(v[j]) : 0u);
-        const float shift = softmax_shift(key_value(wave_max(best)));
+        for (int j = 0; j < J; ++j) part_of[j * 64 + lane] = 0.0f;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        // expert e = lane * J + j stands at j * 64 + lane
+        float *spot = part_of + (id >= 0 ? id % J * 64 + id / J : 0);
+        if (id >= 0) *spot = __int_as_float(lane);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        const bool twice = __any(id >= 0 && __float_as_int(*spot) != lane);
+        float top = v[0];
+#pragma unroll
+        for (int j = 1; j < J; ++j) top = fmaxf(top, v[j]);          // a NaN stays in v
+        const float shift = softmax_shift(key_value(wave_max(order_key(top == top ? top : -INFINITY))));
         float part = 0.0f, pc = 0.0f;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
@@ -407,7 +438,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteArgs
         const float sum = wave_sum(part);
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         float z = wave_sum(pc) * inv;
-        float e = id >= 0 ? exp_neg(logit - shift) : 0.0f;
+        const float e = id >= 0 ? exp_neg(logit - shift) : 0.0f;
         float add;
         if (a.renorm) {
             const float chosen = wave_sum(e);
@@ -417,14 +448,21 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteArgs
             add = e * inv * g;
             z += wave_sum(add);
         }
-#pragma unroll
-        for (int j = 0; j < J; ++j) v[j] = v[j] * inv * (c[j] - z);
-        for (int k = 0; k < a.topk; ++k) {
-            const int expert = __builtin_amdgcn_readlane(id, k);
-            const float x = __uint_as_float(uint32_t(__builtin_amdgcn_readlane(int(__float_as_uint(add)), k)));
-#pragma unroll
-            for (int j = 0; j < J; ++j) v[j] += lane * J + j == expert ? x : 0.0f;
+        __builtin_amdgcn_wave_barrier();
+        if (!twice) {
+            if (id >= 0) *spot = add;
+        } else {
+            if (id >= 0) *spot = 0.0f;
+            for (int k = 0; k < a.topk; ++k) {
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+                if (lane == k && id >= 0) *spot += add;
+            }
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int j = 0; j < J; ++j) v[j] = __builtin_fmaf(v[j] * inv, c[j] - z, part_of[j * 64 + lane]);
         T *row = static_cast<T *>(a.dlogits) + t * a.ldd + lane * J;
         if constexpr (VEC) {
             struct alignas(J * sizeof(T) < 16 ? J * sizeof(T) : 16) Run { T e[J]; };
