@@ -10,6 +10,7 @@
 // lane that has the key, and in it the first, is the lowest expert.
 #include "layer_ops.h"
 #include "wave.cuh"
+#include "../../include/moe_layer.h"
 
 #include <hip/hip_runtime.h>
 
@@ -25,13 +26,12 @@ constexpr int kRouteMaxGroups = 16384;      // workgroups; further tokens in a l
 constexpr int kJoinWaves = 16;
 constexpr int kJoinMaxGroups = 4096;        // workgroups of the joining kernel; further jobs in a loop
 
-// float -> key: ascending like the number, -0 equal to +0, NaN above +inf.
-// No logit's key is 0 (that of -inf is 0x007fffff): 0 marks a place that
+// float -> key: ascending like the number, -0 equal to +0 (a NaN's is to be
+// set by the caller: the largest key, above +inf).  No logit's key is 0 (that of -inf is 0x007fffff): 0 marks a place that
 // holds no expert, or one already taken.
 __device__ __forceinline__ uint32_t order_key(float f) {
     const uint32_t u = __float_as_uint(f + 0.0f);
-    const uint32_t key = u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
-    return f == f ? key : 0xffffffffu;
+    return u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float key_value(uint32_t k) {
     return __uint_as_float(k == 0xffffffffu ? 0x7fffffffu : k ^ (k >> 31 ? 0x80000000u : 0xffffffffu));
@@ -91,70 +91,101 @@ __device__ __forceinline__ void sort_keys(uint32_t (&k)[N]) {
 
 // The topk largest: lane k < topk receives the k-th's expert and logit.
 // Returns the row's largest logit (NaN if the row holds one).
-//   Each lane sorts its keys and puts the list into the wave's LDS (`lists`, 64
-// * (J + 1) keys, place by place, a 0 at its end); it keeps the head and the one behind it. A round
-// takes the largest head (six cross-lane steps) and its lane moves up: 13
-// vector operations a round, against 45 with the lists in registers and the
-// place searched for each time.  Which of the lane's experts it was is found
-// afterwards for all rounds at once, in the row itself: the (times+1)-th that
-// equals the round's logit, `times` being how many of the rounds just before
-// had the same lane and key (equal keys leave a lane one after the other, as
-// the first lane that has the largest key is always the one taken).
+//   Each lane sorts its keys and puts the list into the wave's LDS (`lists`,
+// place by place, a 0 behind it); it keeps the head and the one behind it.  A
+// round takes the largest head (six cross-lane steps), notes it with its lane
+// and moves that lane up: 12 vector operations a round, against 45 with the
+// keys in registers and their place searched for in each round.  Which of the
+// lane's experts it was is found afterwards for all rounds at once, in the row
+// itself: the first that equals the round's logit, or the (times+1)-th where
+// the `times` rounds just before had the same lane and key (equal keys leave a
+// lane one after the other, as the first lane that has the largest key is
+// always the one taken).
+//   The kernel is bound by these operations (424 a row before the last three
+// of the steps above, 11 us at 16,384 rows of 512 on all vector units).
+template <int J> struct Lists {
+    // the last two: the 0, and what a lane taken J times reads.  A row is 64 /
+    // J longer than 64, so that experts in order (place e % J of lane e / J)
+    // lie in different banks.
+    uint32_t place[J + 2][64 + (J > 1 ? 64 / J : 0)];
+    uint32_t round[2 * MOE_ROUTE_MAX_TOPK];   // key and lane of each round
+};
 template <int J, int DT, bool VEC>
 __device__ __forceinline__ float choose(const RouteArgs &a, int64_t row, const float (&v)[J], int lane, int &id,
-                                        float &logit, uint32_t *lists) {
+                                        float &logit, Lists<J> &lists) {
     uint32_t key[J];
+    bool odd = false;                         // NaN in the row, or infinities of both signs
+    {
+        float sum = v[0];
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-        const uint32_t k = order_key(v[j]);
-        key[j] = lane * J + (VEC ? 0 : j) < a.n_expert ? k : 0u;
+        for (int j = 1; j < J; ++j) sum += v[j];
+        odd = __any(sum != sum);
     }
+#pragma unroll
+    for (int j = 0; j < J; ++j) key[j] = order_key(v[j]);
+    if (odd)
+#pragma unroll
+        for (int j = 0; j < J; ++j) key[j] = v[j] == v[j] ? key[j] : 0xffffffffu;
+    if (a.n_expert < 64 * J)
+#pragma unroll
+        for (int j = 0; j < J; ++j) key[j] = lane * J + (VEC ? 0 : j) < a.n_expert ? key[j] : 0u;
     sort_keys(key);
     uint32_t head = key[0], next = 0;
+    __builtin_amdgcn_wave_barrier();
     if constexpr (J > 1) {
         next = key[1];
-        __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int j = 1; j <= J; ++j) lists[j * 64 + lane] = j < J ? key[j] : 0u;
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
+        for (int j = 1; j <= J; ++j) lists.place[j][lane] = j < J ? key[j] : 0u;
     }
-    int at = 1;                          // the place of `next`
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    int at = 1;                               // the place of `next`
     uint32_t first = 0;
-    int mine = 0, from = 0;
     for (int k = 0; k < a.topk; ++k) {
         const uint32_t top = wave_max(head);
-        const int owner = __builtin_ctzll(__ballot(head == top));
-        mine = lane == k ? int(top) : mine;
-        from = lane == k ? owner : from;
+        uint64_t owner = __ballot(head == top);
+        owner &= -owner;
+        const bool taken = __builtin_amdgcn_inverse_ballot_w64(owner);
         first = k == 0 ? top : first;
-        // J rounds at most take from one lane, the last of them finds the 0 at place J
-        const bool taken = lane == owner;
+        if (taken) {
+            lists.round[2 * k] = head;
+            lists.round[2 * k + 1] = uint32_t(lane);
+        }
         head = taken ? next : head;
         if constexpr (J > 1) {
             at += taken;
-            next = lists[min(at, J) * 64 + lane];
+            next = lists.place[at][lane];
         }
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const int k = min(lane, a.topk - 1);
+    const uint32_t mine = lists.round[2 * k];
+    const int from = int(lists.round[2 * k + 1]);
     id = from * J;
-    logit = key_value(uint32_t(mine));
+    logit = key_value(mine);
     if constexpr (J > 1) {
+        float u[J];
+        load_row<J, DT, VEC>(a.logits, row, a.n_expert, from, u);
         int times = 0;
         bool same = lane < a.topk;
         for (int d = 1; d < a.topk; ++d) {
-            const int m = __shfl_up(mine, d), f = __shfl_up(from, d);
-            same = same && lane >= d && m == mine && f == from;
+            const int b = max(k - d, 0);
+            same = same && k >= d && lists.round[2 * b] == mine && int(lists.round[2 * b + 1]) == from;
             if (!__any(same)) break;
             times += same;
         }
-        float u[J];
-        load_row<J, DT, VEC>(a.logits, row, a.n_expert, from, u);
         int place = 0;
+        if (!odd && !__any(times > 0)) {
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const bool hit = (u[j] == logit || (u[j] != u[j] && logit != logit)) && (VEC || from * J + j < a.n_expert);
-            place = hit && times == 0 ? j : place;
-            times -= hit;
+            for (int j = J - 1; j >= 0; --j) place = u[j] == logit ? j : place;
+        } else {
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const bool hit = u[j] == logit || (u[j] != u[j] && logit != logit);
+                place = hit && times == 0 ? j : place;
+                times -= hit;
+            }
         }
         id += place;
     }
@@ -193,7 +224,7 @@ __device__ __forceinline__ int sequence_of(const int32_t *seq_off, int n_seq, in
 // Routes token t; with STATS the row's softmax is added to acc.
 template <int J, int DT, bool VEC, bool STATS>
 __device__ __forceinline__ void route_token(const RouteArgs &a, int t, int lane, bool count,
-                                            float (&acc)[J], int *hist, uint32_t *lists) {
+                                            float (&acc)[J], int *hist, Lists<J> &lists) {
     float v[J];
     load_row<J, DT, VEC>(a.logits, int64_t(t) * a.ld, a.n_expert, lane, v);
     int id;
@@ -231,7 +262,7 @@ __device__ __forceinline__ void route_token(const RouteArgs &a, int t, int lane,
 template <int J, int DT, bool VEC>
 __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
     const int lane = threadIdx.x & 63;
-    __shared__ alignas(16) uint32_t lists[kRouteWaves][64 * (J + 1)];
+    __shared__ Lists<J> lists[kRouteWaves];
     float none[J];
     for (int64_t t = int64_t(blockIdx.x) * kRouteWaves + (threadIdx.x >> 6); t < a.tokens;
          t += int64_t(gridDim.x) * kRouteWaves)
@@ -244,7 +275,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
 template <int J, int DT, bool VEC>
 __global__ __launch_bounds__(64 * balance_waves(J)) void route_balance_kernel(RouteArgs a, BalanceLayout L) {
     constexpr int kWaves = balance_waves(J), kThreads = 64 * kWaves;
-    __shared__ uint32_t red[kWaves][64 * (J + 1)];      // the waves' sums; while routing, their lists
+    __shared__ Lists<J> lists[kWaves];        // while routing; then the waves' sums, from place[0] on
     __shared__ int hist[64 * J];
     if (blockIdx.x == 0 && threadIdx.x == 0) *reinterpret_cast<int32_t *>(a.ws + L.done) = 0;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -271,19 +302,20 @@ __global__ __launch_bounds__(64 * balance_waves(J)) void route_balance_kernel(Ro
             }
         }
         for (int t = pos + wave; t < end; t += kWaves)
-            route_token<J, DT, VEC, true>(a, t, lane, inside, acc, hist, red[wave]);
+            route_token<J, DT, VEC, true>(a, t, lane, inside, acc, hist, lists[wave]);
         if (inside) {
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-                red[wave][lane * J + j] = __float_as_uint(acc[j]);
+                lists[wave].place[j][lane] = __float_as_uint(acc[j]);
                 acc[j] = 0.0f;
             }
             __syncthreads();
             const size_t at = (size_t(blockIdx.x) + s) * a.n_expert;
             for (int e = threadIdx.x; e < a.n_expert; e += kThreads) {
-                float p = __uint_as_float(red[0][e]);
+                const int j = e % J, l = e / J;
+                float p = __uint_as_float(lists[0].place[j][l]);
 #pragma unroll
-                for (int w = 1; w < kWaves; ++w) p += __uint_as_float(red[w][e]);
+                for (int w = 1; w < kWaves; ++w) p += __uint_as_float(lists[w].place[j][l]);
                 out_p[at + e] = p;
                 out_c[at + e] = hist[e];
                 hist[e] = 0;
