@@ -68,77 +68,78 @@ def _load_torch():
     return _torch
 
 
+def _current(stream, t, what: str):
+    """The current device, which has to hold t, and the raw stream (torch's current one by
+    default).  A call is a few microseconds, most of them this module's: hence raw handles and
+    few calls per tensor."""
+    c = _load_torch()._C
+    device = t.get_device() if t is not None and t.is_cuda else -1
+    if device < 0 or device != c._cuda_getDevice():
+        raise MoeError(-1, f"{what}: {'None' if t is None else t.device} is not the current device")
+    if stream is None:
+        return device, c._cuda_getCurrentRawStream(device)
+    return device, stream if isinstance(stream, int) else stream.cuda_stream
+
+
 def _dtype(t, what: str) -> int:
-    _load_torch()
     code = _codes.get(t.dtype)
     if code is None:
         raise MoeError(-3, f"{what}: {t.dtype}")
     return code
 
 
-def _stream(stream):
-    """The raw stream, torch's current one by default."""
-    if stream is None:
-        c = _load_torch()._C
-        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
-    return _lib._stream(stream)
-
-
-def _address(t, what: str):
-    device = t.get_device()
-    if device < 0 or not t.is_cuda:
-        raise MoeError(-1, f"{what}: on {t.device}, not in device memory")
-    if device != _load_torch()._C._cuda_getDevice():
-        raise MoeError(-1, f"{what}: on {t.device}, the current device is cuda:{_load_torch()._C._cuda_getDevice()}")
+def _place(device: int, t, what: str):
+    """The address of a tensor on the current device."""
+    if t.get_device() != device or device < 0:
+        raise MoeError(-1, f"{what}: on {t.device}, the current device is cuda:{device}")
     return t.data_ptr()
 
 
-def _arg(t, what: str, dtype, shape):
-    """A dense tensor of the given type and shape on the current device -> its address."""
+def _dense(device: int, t, what: str, dtype, shape):
+    """The address of a dense tensor of the given type and shape (None: no tensor)."""
     if t is None:
         return None
     if t.dtype != dtype:
         raise MoeError(-3, f"{what}: {t.dtype} instead of {dtype}")
     if t.shape != shape or not t.is_contiguous():
         raise MoeError(-1, f"{what}: shape {tuple(t.shape)}, strides {t.stride()}; dense {tuple(shape)} wanted")
-    return _address(t, what)
+    if t.get_device() == device and device >= 0:
+        return t.data_ptr()
+    return _place(device, t, what)
 
 
-def _rows(t, what: str, shape):
-    """A matrix with dense rows -> its address and row stride in elements."""
-    if t.shape != shape or (t.stride(1) != 1 and shape[1] > 1):
+def _rows(device: int, t, what: str, shape, written: bool = False):
+    """The address and row stride of a matrix with dense rows (that do not overlap, if written)."""
+    ld, step = t.stride() if t.dim() == 2 else (0, 0)
+    if t.shape != shape or (step != 1 and shape[1] > 1) or (written and ld < shape[1] and shape[0] > 1):
         raise MoeError(-1, f"{what}: shape {tuple(t.shape)}, strides {t.stride()}; {tuple(shape)} with dense rows wanted")
     # the stride of a single row says nothing: torch may give it any value
-    return _address(t, what), t.stride(0) if shape[0] > 1 else shape[1]
-
-
-def _out_of_place(t, what: str):
-    """Rows that are written: no two of them may overlap."""
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise MoeError(-1, f"{what}: rows overlap (strides {t.stride()})")
-
-
-def _route(logits, topk: int, renorm: bool, scale: float):
-    if logits.dim() != 2:
-        raise MoeError(-1, f"logits: shape {tuple(logits.shape)}")
-    T, E = logits.shape
-    ptr, ld = _rows(logits, "logits", (T, E))
-    return (ptr, ld, _dtype(logits, "logits"), T, E, topk, MOE_ROUTE_RENORM if renorm else 0, scale)
+    return _place(device, t, what), ld if shape[0] > 1 else shape[1]
 
 
 def _matrix(t, what: str):
-    if t.dim() != 2:
-        raise MoeError(-1, f"{what}: shape {tuple(t.shape)}")
+    if t is None or t.dim() != 2:
+        raise MoeError(-1, f"{what}: {None if t is None else tuple(t.shape)} is not a matrix")
     return t.shape
+
+
+def _route(device: int, logits, topk: int, renorm: bool, scale: float):
+    T, E = _matrix(logits, "logits")
+    ptr, ld = _rows(device, logits, "logits", (T, E))
+    return (ptr, ld, _dtype(logits, "logits"), T, E, topk, MOE_ROUTE_RENORM if renorm else 0, scale)
 
 
 def moe_route(logits, ids, w, renorm: bool = True, scale: float = 1.0, stream=None):
     """logits [T, E] (fp32, bf16 or fp16, dense rows) -> ids int32 [T, topk], w fp32 [T, topk]."""
     torch = _load_torch()
-    T, K = _matrix(ids, "ids")
-    head = _route(logits, K, renorm, scale)
-    _lib._check(lib().moe_route(*head, _arg(ids, "ids", torch.int32, (head[3], K)),
-                                _arg(w, "w", torch.float32, (head[3], K)), _stream(stream)), "moe_route")
+    dev, raw = _current(stream, logits, "logits")
+    K = _matrix(ids, "ids")[1]
+    head = _route(dev, logits, K, renorm, scale)
+    shape = (head[3], K)
+    st = lib().moe_route(*head, _dense(dev, ids, "ids", torch.int32, shape),
+                         _dense(dev, w, "w", torch.float32, shape), raw)
+    if st:
+        raise MoeError(st, "moe_route")
 
 
 def moe_balance_bytes(tokens: int, n_expert: int, n_seq: int) -> int:
@@ -150,15 +151,24 @@ def moe_route_balance(logits, seq_off, coef: float, ids, w, counts, probs, loss,
     """moe_route with the balance statistics of the sequences seq_off (int32 [S+1]) bounds:
     counts int32 [S, E], probs fp32 [S, E], loss fp32 [1]."""
     torch = _load_torch()
-    T, K = _matrix(ids, "ids")
-    head = _route(logits, K, renorm, scale)
+    dev, raw = _current(stream, logits, "logits")
+    K = _matrix(ids, "ids")[1]
+    head = _route(dev, logits, K, renorm, scale)
     T, E, S = head[3], head[4], seq_off.numel() - 1
     f32, i32 = torch.float32, torch.int32
-    _lib._check(lib().moe_route_balance(
-        *head, _arg(seq_off, "seq_off", i32, (S + 1,)), S, coef, _arg(ids, "ids", i32, (T, K)),
-        _arg(w, "w", f32, (T, K)), _arg(counts, "counts", i32, (S, E)), _arg(probs, "probs", f32, (S, E)),
-        _arg(loss, "loss", f32, (1,)), _address(workspace, "workspace"),
-        workspace.numel() * workspace.element_size(), _stream(stream)), "moe_route_balance")
+    st = lib().moe_route_balance(
+        *head, _dense(dev, seq_off, "seq_off", i32, (S + 1,)), S, coef, _dense(dev, ids, "ids", i32, (T, K)),
+        _dense(dev, w, "w", f32, (T, K)), _dense(dev, counts, "counts", i32, (S, E)),
+        _dense(dev, probs, "probs", f32, (S, E)), _dense(dev, loss, "loss", f32, (1,)),
+        *_workspace(dev, workspace), raw)
+    if st:
+        raise MoeError(st, "moe_route_balance")
+
+
+def _workspace(device: int, t):
+    if not t.is_contiguous():
+        raise MoeError(-1, f"workspace: strides {t.stride()}")
+    return _place(device, t, "workspace"), t.numel() * t.element_size()
 
 
 def moe_route_backward(logits, ids, dw, dlogits, renorm: bool = True, scale: float = 1.0, seq_off=None,
@@ -167,34 +177,36 @@ def moe_route_backward(logits, ids, dw, dlogits, renorm: bool = True, scale: flo
     (seq_off and counts of the forward call, dloss fp32 [1] or None for 1) -> dlogits, the
     logits' type and shape."""
     torch = _load_torch()
-    T, K = _matrix(ids, "ids")
-    head = _route(logits, K, renorm, scale)
+    dev, raw = _current(stream, logits, "logits")
+    K = _matrix(ids, "ids")[1]
+    head = _route(dev, logits, K, renorm, scale)
     T, E = head[3], head[4]
     S = 0 if seq_off is None else seq_off.numel() - 1
     f32, i32 = torch.float32, torch.int32
     if dlogits.dtype != logits.dtype:
         raise MoeError(-3, f"dlogits: {dlogits.dtype} instead of {logits.dtype}")
-    d_ptr, ldd = _rows(dlogits, "dlogits", (T, E))
-    _out_of_place(dlogits, "dlogits")
-    _lib._check(lib().moe_route_backward(
-        *head, _arg(ids, "ids", i32, (T, K)), _arg(dw, "dw", f32, (T, K)),
-        _arg(seq_off, "seq_off", i32, (S + 1,)), S, coef, _arg(counts, "counts", i32, (S, E)),
-        _arg(dloss, "dloss", f32, (1,)), d_ptr, ldd, _stream(stream)), "moe_route_backward")
+    d_ptr, ldd = _rows(dev, dlogits, "dlogits", (T, E), True)
+    st = lib().moe_route_backward(
+        *head, _dense(dev, ids, "ids", i32, (T, K)), _dense(dev, dw, "dw", f32, (T, K)),
+        _dense(dev, seq_off, "seq_off", i32, (S + 1,)), S, coef, _dense(dev, counts, "counts", i32, (S, E)),
+        _dense(dev, dloss, "dloss", f32, (1,)), d_ptr, ldd, raw)
+    if st:
+        raise MoeError(st, "moe_route_backward")
 
 
 def moe_combine_backward(dm, w, dout, dw, ddm=None, stream=None):
     """The gradient of moe_combine: dout fp32 [T, H] -> dw fp32 [T, topk] and ddm fp32
     [T*topk, H] (either may be None; dm is read for dw, w [T, topk] for ddm)."""
     f32 = _load_torch().float32
+    dev, raw = _current(stream, dout, "dout")
     T, H = _matrix(dout, "dout")
-    of = dw if dw is not None else w
-    if of is None:
-        raise MoeError(-1, "moe_combine_backward: neither dw nor w")
-    K = _matrix(of, "dw" if dw is not None else "w")[1]
-    _lib._check(lib().moe_combine_backward(
-        _arg(dm, "dm", f32, (T * K, H)), _arg(w, "w", f32, (T, K)), _arg(dout, "dout", f32, (T, H)),
-        T, K, H, _arg(dw, "dw", f32, (T, K)), _arg(ddm, "ddm", f32, (T * K, H)), _stream(stream)),
-        "moe_combine_backward")
+    K = _matrix(dw if dw is not None else w, "dw or w")[1]
+    rows, per = (T * K, H), (T, K)
+    st = lib().moe_combine_backward(
+        _dense(dev, dm, "dm", f32, rows), _dense(dev, w, "w", f32, per), _dense(dev, dout, "dout", f32, (T, H)),
+        T, K, H, _dense(dev, dw, "dw", f32, per), _dense(dev, ddm, "ddm", f32, rows), raw)
+    if st:
+        raise MoeError(st, "moe_combine_backward")
 
 
 class AdapterSet:
@@ -211,30 +223,35 @@ class AdapterSet:
         code = _dtype(a, "a")
         if code == MOE_F32:
             raise MoeError(-3, f"a: {a.dtype}")
+        dev = a.get_device() if a.is_cuda else -1
         self.tensors = (a, b, scale, rank)
-        self.n_in, self.n_out, self.rank = n_in, n_out, r
+        self.device, self.n_in, self.n_out, self.rank = dev, n_in, n_out, r
         self.struct = moe_adapter_set(
-            code, n, r, n_in, n_out, _arg(a, "a", a.dtype, (n, r, n_in)), _arg(b, "b", a.dtype, (n, n_out, r)),
-            _arg(scale, "scale", torch.float32, (n,)), _arg(rank, "rank", torch.int32, (n,)))
+            code, n, r, n_in, n_out, _dense(dev, a, "a", a.dtype, (n, r, n_in)),
+            _dense(dev, b, "b", a.dtype, (n, n_out, r)), _dense(dev, scale, "scale", torch.float32, (n,)),
+            _dense(dev, rank, "rank", torch.int32, (n,)))
+        self.ref = ctypes.byref(self.struct)
 
 
 def moe_adapters_bytes(adapters: AdapterSet, tokens: int) -> int:
-    return int(lib().moe_adapters_bytes(ctypes.byref(adapters.struct), tokens))
+    return int(lib().moe_adapters_bytes(adapters.ref, tokens))
 
 
 def moe_adapters(adapters: AdapterSet, ids, x, base, out, workspace, stream=None):
     """out = base + each row's adapter over x: ids int32 [T] (negative: none), x [T, n_in], base
     and out [T, n_out] of fp32 or the set's type, dense rows; out may be base."""
     torch = _load_torch()
-    _address(adapters.tensors[0], "adapters")
+    dev, raw = _current(stream, x, "x")
+    if adapters.device != dev:
+        raise MoeError(-1, f"adapters: on cuda:{adapters.device}, the current device is cuda:{dev}")
     T = ids.numel()
-    x_ptr, ldx = _rows(x, "x", (T, adapters.n_in))
-    b_ptr, ldb = _rows(base, "base", (T, adapters.n_out))
-    o_ptr, ldo = _rows(out, "out", (T, adapters.n_out))
-    _out_of_place(out, "out")
-    if not (x.dtype == base.dtype == out.dtype):
+    kind = x.dtype
+    if base.dtype != kind or out.dtype != kind:
         raise MoeError(-3, f"moe_adapters: x {x.dtype}, base {base.dtype}, out {out.dtype}")
-    _lib._check(lib().moe_adapters(
-        ctypes.byref(adapters.struct), _arg(ids, "ids", torch.int32, (T,)), T, _dtype(x, "x"), x_ptr, ldx,
-        b_ptr, ldb, o_ptr, ldo, _address(workspace, "workspace"),
-        workspace.numel() * workspace.element_size(), _stream(stream)), "moe_adapters")
+    shape = (T, adapters.n_out)
+    st = lib().moe_adapters(
+        adapters.ref, _dense(dev, ids, "ids", torch.int32, (T,)), T, _dtype(x, "x"),
+        *_rows(dev, x, "x", (T, adapters.n_in)), *_rows(dev, base, "base", shape),
+        *_rows(dev, out, "out", shape, True), *_workspace(dev, workspace), raw)
+    if st:
+        raise MoeError(st, "moe_adapters")

@@ -286,3 +286,41 @@ def test_same_bits_every_time():
     for other in outs[1:]:
         for a, b in zip(outs[0], other):
             assert torch.equal(a.view(torch.int32), b.view(torch.int32))
+
+
+def test_binding_refusals():
+    """What only the binding can see: types, shapes, strides and places of tensors."""
+    l, ids, w = torch.zeros(4, 8, device="cuda"), torch.zeros(4, 2, dtype=torch.int32, device="cuda"), \
+        torch.zeros(4, 2, device="cuda")
+
+    def status(f, *a, **k):
+        with pytest.raises(moe.MoeError) as e:
+            f(*a, **k)
+        return e.value.status
+
+    assert status(moe.moe_route, l.double(), ids, w) == -3
+    assert status(moe.moe_route, l, ids.long(), w) == -3
+    assert status(moe.moe_route, l, ids, w.half()) == -3
+    assert status(moe.moe_route, l.cpu(), ids, w) == -1
+    assert status(moe.moe_route, l, ids.cpu(), w) == -1
+    assert status(moe.moe_route, l, ids, None) == -1
+    assert status(moe.moe_route, l[0], ids, w) == -1
+    assert status(moe.moe_route, l.t(), ids, w) == -1                        # rows not dense
+    assert status(moe.moe_route, l, ids[:3], w) == -1
+    assert status(moe.moe_route, l, ids, torch.zeros(2, 4, device="cuda").t()) == -1
+    one = torch.zeros(1, 8, device="cuda").expand(4, 8)
+    assert status(moe.moe_route_backward, l, ids, w, one) == -1              # rows written over one another
+    assert status(moe.moe_route_backward, l, ids, w, l.half()) == -3
+    assert status(moe.moe_combine_backward, l, w, l, w[:, :1].contiguous()) == -1
+    assert status(moe.moe_route, one, ids, w) == -1                          # ld < n_expert
+    a = torch.zeros(2, 16, 64, device="cuda", dtype=torch.bfloat16)
+    s = moe.AdapterSet(a, torch.zeros(2, 32, 16, device="cuda", dtype=torch.bfloat16), torch.ones(2, device="cuda"))
+    x, y, i = torch.zeros(4, 64, device="cuda"), torch.zeros(4, 32, device="cuda"), ids[:, 0].contiguous()
+    ws = torch.empty(moe.moe_adapters_bytes(s, 4), dtype=torch.uint8, device="cuda")
+    assert status(moe.moe_adapters, s, i, x.half(), y.half(), y.half(), ws) == -3      # the set is bf16
+    assert status(moe.moe_adapters, s, i, x, y.bfloat16(), y, ws) == -3
+    assert status(moe.moe_adapters, s, i[:3], x, y, y, ws) == -1
+    assert status(moe.moe_adapters, s, i, x, y, y.clone()[:1].expand(4, 32), ws) == -1
+    assert status(moe.moe_adapters, s, i, x, y, y, ws[:-16]) == -4
+    assert status(moe.AdapterSet, a, torch.zeros(2, 32, 8, device="cuda", dtype=torch.bfloat16),
+                  torch.ones(2, device="cuda")) == -1
