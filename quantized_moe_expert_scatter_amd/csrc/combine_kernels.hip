@@ -15,12 +15,16 @@
 // The combine's gradient reads the same rows once more: a token's output
 // gradient against each of its K rows (the routing weights' gradient), and
 // times each weight (the rows' gradient).  It is bound by HBM too: K + 1 rows
-// read per token, K written.
+// read per token, K written.  2,048 tokens, top-10 of 2560: 231 MB in 35 us
+// (6.5 TB/s); 8,192 with the rows' gradient: 1,762 MB in 319 us (5.5 TB/s,
+// what a large copy reaches).
 #include "internal.h"
 #include "layer_ops.h"
 #include "wave.cuh"
 
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 namespace moe {
 
@@ -28,6 +32,10 @@ namespace {
 
 constexpr int kCombineThreads = 256;   // one float4 of one token per thread, over the flat range
 constexpr int kCombineBatch = 16;      // slots whose loads are issued together (all of top-10)
+
+constexpr int kBackwardRows = 8;       // rows of a token that one wave of the gradient takes at most
+constexpr int kBackwardFewJobs = 2048; // fewer (token, rows) jobs share their columns over four waves
+                                       // (at 4,096 jobs: 38.1 us shared, 34.4 not)
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
@@ -72,53 +80,71 @@ __global__ __launch_bounds__(kCombineThreads) void combine_kernel(const float *d
     else *dst = acc;
 }
 
-// One wave per token: the output gradient's chunk stays in registers while the
-// K rows' chunks pass; the K sums are joined over the lanes at the end.
-template <bool DW, bool DDM>
+// NB rows of one token per wave (all of them clamped to the last, so that their
+// loads are in flight together): the output gradient's chunk stays in registers
+// while the rows' chunks pass; the NB sums are joined over the lanes at the end.
+// SPLIT: few tokens, the four waves of a workgroup share the columns of the
+// same rows and are added through LDS.
+template <int NB, bool DW, bool DDM, bool SPLIT, bool STREAM>
 __global__ __launch_bounds__(kCombineThreads) void combine_backward_kernel(const float *dm, const float *w,
                                                                            const float *dout, int tokens,
-                                                                           int topk, int h4, float *dw,
-                                                                           float *ddm) {
-    const int lane = threadIdx.x & 63;
-    const int64_t t = int64_t(blockIdx.x) * (kCombineThreads / 64) + (threadIdx.x >> 6);
-    if (t >= tokens) return;
-    const f32x4 *g4 = reinterpret_cast<const f32x4 *>(dout) + size_t(t) * h4;
-    for (int k0 = 0; k0 < topk; k0 += kCombineBatch) {
-        const int nk = min(kCombineBatch, topk - k0);
-        const size_t row = (size_t(t) * topk + k0) * h4;
-        const f32x4 *src = reinterpret_cast<const f32x4 *>(dm) + row;
-        f32x4 *dst = reinterpret_cast<f32x4 *>(ddm) + row;
-        float acc[kCombineBatch];
+                                                                           int topk, int h4, int groups,
+                                                                           float *dw, float *ddm) {
+    __shared__ float red[SPLIT ? 4 : 1][NB];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t job = SPLIT ? int64_t(blockIdx.x) : int64_t(blockIdx.x) * 4 + wave;
+    if (job >= int64_t(tokens) * groups) return;
+    const int64_t t = job / groups;
+    const int k0 = int(job % groups) * NB;
+    const f32x4 *g4 = reinterpret_cast<const f32x4 *>(dout) + t * h4;
+    int64_t row[NB];
+    float wk[NB], acc[NB];
 #pragma unroll
-        for (int j = 0; j < kCombineBatch; ++j) acc[j] = 0.0f;
-        for (int c = lane; c < h4; c += 64) {
-            const f32x4 g = g4[c];
+    for (int j = 0; j < NB; ++j) {
+        row[j] = t * topk + min(k0 + j, topk - 1);
+        if constexpr (DDM) wk[j] = w[row[j]];
+        acc[j] = 0.0f;
+    }
+    const int step = SPLIT ? 256 : 64;
+#pragma unroll 2
+    for (int c = SPLIT ? wave * 64 + lane : lane; c < h4; c += step) {
+        const f32x4 g = g4[c];
+        f32x4 d[NB];
+        if constexpr (DW)
 #pragma unroll
-            for (int j = 0; j < kCombineBatch; ++j)
-                if (j < nk) {
-                    if constexpr (DW) {
-                        const f32x4 d = src[size_t(j) * h4 + c];
-                        acc[j] = __builtin_fmaf(g.x, d.x, acc[j]);
-                        acc[j] = __builtin_fmaf(g.y, d.y, acc[j]);
-                        acc[j] = __builtin_fmaf(g.z, d.z, acc[j]);
-                        acc[j] = __builtin_fmaf(g.w, d.w, acc[j]);
-                    }
-                    if constexpr (DDM) {
-                        const float wk = w[t * topk + k0 + j];
-                        dst[size_t(j) * h4 + c] = f32x4{wk * g.x, wk * g.y, wk * g.z, wk * g.w};
-                    }
+            for (int j = 0; j < NB; ++j)
+                d[j] = load4<STREAM>(reinterpret_cast<const f32x4 *>(dm) + row[j] * h4 + c);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            if constexpr (DW) {
+                acc[j] = __builtin_fmaf(g.x, d[j].x, acc[j]);
+                acc[j] = __builtin_fmaf(g.y, d[j].y, acc[j]);
+                acc[j] = __builtin_fmaf(g.z, d[j].z, acc[j]);
+                acc[j] = __builtin_fmaf(g.w, d[j].w, acc[j]);
+            }
+            if constexpr (DDM) {
+                f32x4 *dst = reinterpret_cast<f32x4 *>(ddm) + row[j] * h4 + c;
+                const f32x4 v = {wk[j] * g.x, wk[j] * g.y, wk[j] * g.z, wk[j] * g.w};
+                if (k0 + j < topk) {
+                    if constexpr (STREAM) __builtin_nontemporal_store(v, dst);
+                    else *dst = v;
                 }
+            }
         }
-        if constexpr (DW) {
-            float mine = 0.0f;
+    }
+    if constexpr (DW) {
+        float mine = 0.0f;
 #pragma unroll
-            for (int j = 0; j < kCombineBatch; ++j)
-                if (j < nk) {
-                    const float s = wave_sum(acc[j]);
-                    mine = lane == j ? s : mine;
-                }
-            if (lane < nk) dw[t * topk + k0 + lane] = mine;
+        for (int j = 0; j < NB; ++j) {
+            const float s = wave_sum(acc[j]);
+            mine = lane == j ? s : mine;
         }
+        if constexpr (SPLIT) {
+            if (lane < NB) red[wave][lane] = mine;
+            __syncthreads();
+            if (wave == 0 && lane < NB) mine = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+        }
+        if ((!SPLIT || wave == 0) && lane < NB && k0 + lane < topk) dw[t * topk + k0 + lane] = mine;
     }
 }
 
@@ -127,17 +153,42 @@ __global__ __launch_bounds__(kCombineThreads) void combine_backward_kernel(const
 hipError_t launch_combine_backward(const float *dm, const float *w, const float *dout, int tokens,
                                    int topk, int hidden, float *dw, float *ddm, hipStream_t stream) {
     const int h4 = hidden / 4;
-    const dim3 grid(unsigned((int64_t(tokens) + 3) / 4)), block(kCombineThreads);
-    if (dw && ddm)
-        hipLaunchKernelGGL((combine_backward_kernel<true, true>), grid, block, 0, stream, dm, w, dout,
-                           tokens, topk, h4, dw, ddm);
-    else if (dw)
-        hipLaunchKernelGGL((combine_backward_kernel<true, false>), grid, block, 0, stream, dm, w, dout,
-                           tokens, topk, h4, dw, ddm);
-    else
-        hipLaunchKernelGGL((combine_backward_kernel<false, true>), grid, block, 0, stream, dm, w, dout,
-                           tokens, topk, h4, dw, ddm);
-    return hipGetLastError();
+    // as few groups of at most kBackwardRows rows as there are, of equal size
+    const int groups = (topk + kBackwardRows - 1) / kBackwardRows;
+    const int nb = (topk + groups - 1) / groups;
+    const int64_t jobs = int64_t(tokens) * groups;
+    const bool split = jobs < kBackwardFewJobs;
+    // rows that do not fit the L2s (8 x 4 MB) pass them by.  Top-10 of 2560, dw
+    // alone, normal / past the caches: 26 MB 4.2 / 4.7 us read again at once and
+    // 7.1 / 7.2 from memory; 52 MB 10.8 / 9.1 and 12.4 / 11.8; 210 MB 34.4 / 34.5
+    // and 41.2 / 35.8.
+    const bool big = size_t(tokens) * size_t(topk) * size_t(hidden) * 4u > (size_t(32) << 20);
+    const dim3 grid(unsigned(split ? jobs : (jobs + 3) / 4)), block(kCombineThreads);
+    auto go = [&](auto NB, auto DW, auto DDM, auto SPLIT, auto STREAM) {
+        hipLaunchKernelGGL((combine_backward_kernel<NB.value, DW.value, DDM.value, SPLIT.value, STREAM.value>), grid,
+                           block, 0, stream, dm, w, dout, tokens, topk, h4, groups, dw, ddm);
+        return hipGetLastError();
+    };
+    auto flag = [](bool b, auto f) { return b ? f(std::true_type{}) : f(std::false_type{}); };
+    auto with = [&](auto NB) {
+        return flag(split, [&](auto SPLIT) {
+            return flag(big && !split, [&](auto STREAM) {
+                if (dw && ddm) return go(NB, std::true_type{}, std::true_type{}, SPLIT, STREAM);
+                if (dw) return go(NB, std::true_type{}, std::false_type{}, SPLIT, STREAM);
+                return go(NB, std::false_type{}, std::true_type{}, SPLIT, STREAM);
+            });
+        });
+    };
+    switch (nb) {
+        case 1: return with(std::integral_constant<int, 1>{});
+        case 2: return with(std::integral_constant<int, 2>{});
+        case 3: return with(std::integral_constant<int, 3>{});
+        case 4: return with(std::integral_constant<int, 4>{});
+        case 5: return with(std::integral_constant<int, 5>{});
+        case 6: return with(std::integral_constant<int, 6>{});
+        case 7: return with(std::integral_constant<int, 7>{});
+        default: return with(std::integral_constant<int, 8>{});
+    }
 }
 
 hipError_t launch_combine(const float *dm, const float *w, int tokens, int topk, int hidden,
