@@ -222,31 +222,44 @@ struct TileRows {
 // rows of several adapters passes over x once for each; gridDim.z workgroups
 // share those passes.  The matrix unit's rows are rank rows, its columns rows
 // of x, so whatever a row holds stays in its column.
+//   a and x are loaded row segment by row segment, neighbouring lanes next to
+// each other, and turn through the wave's part of LDS into the matrix unit's
+// layout.  (Loaded in that layout, neighbouring lanes are in different rows and
+// the address unit takes 64 accesses for a load instead of 16; fp32 x came down
+// from 59 to 44 us by this at 16,384 rows of 2560 and rank 64, a from 6.8 to 5.4
+// us at 2,047 fp16 rows and rank 24.)  At 16,384 rows it reads x at 4.1 TB/s:
+// 30 us with a's loads left out, 33 with x's, of 42; more rows or workgroups in
+// flight, deeper prefetch and other shares of the contraction are level.
 template <int XT, int WT, int NR, int MR>
 __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterArgs g, AdapterSplit s) {
     constexpr int kXP = XT == kF32 ? 3 : 1;
-    constexpr int kLoads = XT == kF32 ? 2 * MR : MR;     // 16-byte loads of x per lane and step
+    using T = typename Elem<XT>::T;
+    constexpr int kLanes = XT == kF32 ? 8 : 4;           // lanes of a row's 32 values
+    constexpr int kLoads = 16 * MR * kLanes / 64;        // 16-byte loads of x per lane and step
+    constexpr int kRun = 32 / kLanes;
+    // rows of 32 values and 16 bytes: 16 lanes reading 16 bytes of 16 rows meet no bank twice
+    struct Turn {
+        uint16_t w[16 * NR][32 + 8];
+        T x[16 * MR][32 + 16 / sizeof(T)];
+    };
     __shared__ union {
         f32x4 red[4][NR][MR][64];
-        float x[XT == kF32 ? 4 : 1][16 * MR][36];
+        Turn turn[4];
     } lds;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t first = int64_t(blockIdx.x / s.splits) * (16 * MR);
     const int plane = int(blockIdx.x % s.splits);
     const int r0 = int(blockIdx.y) * 16 * NR;
-    const int k0 = plane * s.slice + wave * 32 + (lane >> 4) * 8;
+    const int k0 = plane * s.slice + wave * 32 + (lane & 3) * 8;          // of a, as loaded
     const int k1 = min(g.n_in, (plane + 1) * s.slice);
     TileRows rows(g, first, 16 * MR, lane);
-    // x, 32 values of every row a step.  fp32: a load takes 8 rows' 128 bytes
-    // and the values turn through the wave's part of LDS; 16-bit: 16 rows' 64
-    // bytes, already in the matrix unit's layout.
-    const int kx = plane * s.slice + wave * 32 + (XT == kF32 ? (lane & 7) * 4 : (lane >> 4) * 8);
-    int64_t x_at[kLoads];
+    const int kx = plane * s.slice + wave * 32 + lane % kLanes * kRun;
+    const T *x_at[kLoads];
 #pragma unroll
-    for (int m = 0; m < kLoads; ++m) {
-        const int64_t t = first + (XT == kF32 ? m * 8 + (lane >> 3) : m * 16 + (lane & 15));
-        x_at[m] = min(t, int64_t(g.tokens) - 1) * g.ldx;
-    }
+    for (int m = 0; m < kLoads; ++m)
+        x_at[m] = static_cast<const T *>(g.x) +
+                  min(first + m * (64 / kLanes) + lane / kLanes, int64_t(g.tokens) - 1) * g.ldx;
+    Turn &turn = lds.turn[wave];
     for (int pass = 0, a; (a = rows.next()) >= 0; ++pass) {
         if (pass % int(gridDim.z) != int(blockIdx.z)) continue;
         if (r0 > 0 && r0 >= rank_of(g, a)) continue;
@@ -254,7 +267,7 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterArgs g, A
         const uint16_t *a_row[NR];
 #pragma unroll
         for (int n = 0; n < NR; ++n)
-            a_row[n] = mat + int64_t(min(r0 + n * 16 + (lane & 15), g.rank - 1)) * g.n_in;
+            a_row[n] = mat + int64_t(min(r0 + n * 16 + (lane >> 2), g.rank - 1)) * g.n_in;
         f32x4 acc[NR][MR];
 #pragma unroll
         for (int n = 0; n < NR; ++n)
@@ -270,40 +283,38 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterArgs g, A
             const int kv = kx + step * kAdapterStep, kvc = kv < k1 ? kv : 0;
 #pragma unroll
             for (int n = 0; n < NR; ++n) q.w[n] = *reinterpret_cast<const u32x4 *>(a_row[n] + kc);
-            using T = typename Elem<XT>::T;
 #pragma unroll
-            for (int m = 0; m < kLoads; ++m)
-                q.x[m] = *reinterpret_cast<const u32x4 *>(static_cast<const T *>(g.x) + x_at[m] + kvc);
+            for (int m = 0; m < kLoads; ++m) q.x[m] = *reinterpret_cast<const u32x4 *>(x_at[m] + kvc);
         };
         auto multiply = [&](const Step &q, int step) {
-            const bool in = k0 + step * kAdapterStep < k1;
+            const bool in = k0 + step * kAdapterStep < k1, x_in = kx + step * kAdapterStep < k1;
             const u32x4 zero = {0, 0, 0, 0};
-            if constexpr (XT == kF32) {
-                const bool x_in = kx + step * kAdapterStep < k1;
-                __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_wave_barrier();
 #pragma unroll
-                for (int m = 0; m < kLoads; ++m)
-                    *reinterpret_cast<u32x4 *>(&lds.x[wave][m * 8 + (lane >> 3)][(lane & 7) * 4]) =
-                        x_in ? q.x[m] : zero;
-                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-                __builtin_amdgcn_wave_barrier();
-            }
+            for (int n = 0; n < NR; ++n)
+                *reinterpret_cast<u32x4 *>(&turn.w[n * 16 + (lane >> 2)][(lane & 3) * 8]) = in ? q.w[n] : zero;
+#pragma unroll
+            for (int m = 0; m < kLoads; ++m)
+                *reinterpret_cast<u32x4 *>(&turn.x[m * (64 / kLanes) + lane / kLanes][lane % kLanes * kRun]) =
+                    x_in ? q.x[m] : zero;
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
             u32x4 v[MR][kXP];
 #pragma unroll
             for (int m = 0; m < MR; ++m) {
+                const T *src = &turn.x[m * 16 + (lane & 15)][(lane >> 4) * 8];
                 if constexpr (XT == kF32) {
                     float f[8];
-                    const float *src = &lds.x[wave][m * 16 + (lane & 15)][(lane >> 4) * 8];
                     *reinterpret_cast<f32x4 *>(f) = *reinterpret_cast<const f32x4 *>(src);
                     *reinterpret_cast<f32x4 *>(f + 4) = *reinterpret_cast<const f32x4 *>(src + 4);
                     split<3>(f, v[m]);
                 } else {
-                    v[m][0] = in ? q.x[m] : zero;
+                    v[m][0] = *reinterpret_cast<const u32x4 *>(src);
                 }
             }
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
-                const u32x4 raw = in ? q.w[n] : zero;
+                const u32x4 raw = *reinterpret_cast<const u32x4 *>(&turn.w[n * 16 + (lane & 15)][(lane >> 4) * 8]);
                 if constexpr (XT == kF16) {
 #pragma unroll
                     for (int m = 0; m < MR; ++m) acc[n][m] = mfma_f16(raw, v[m][0], acc[n][m]);
@@ -317,7 +328,7 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterArgs g, A
         };
         Step one, two;
         load(one, 0);
-        const int steps = (k1 - (k0 - (lane >> 4) * 8) + kAdapterStep - 1) / kAdapterStep;
+        const int steps = (k1 - (k0 - (lane & 3) * 8) + kAdapterStep - 1) / kAdapterStep;
         for (int q = 0; q < steps; q += 2) {
             load(two, q + 1);
             multiply(one, q);
