@@ -200,13 +200,54 @@ __device__ __forceinline__ f32x4 mfma_parts(const u32x4 (&w)[WP], const u32x4 (&
     return c;
 }
 
-// Rows of a tile and their adapters, the same in every wave: lane l has row l.
+// Which rows a tile has.  Up to kSortRows rows (a batch of new tokens, every
+// row its own adapter, where a tile of 16 rows would take up to 16 passes) the
+// tiles take the rows by adapter: each workgroup ranks all rows by (adapter,
+// row), the same way in every workgroup, unless the ids change no more often
+// than there are tiles.  A row's result does not depend on its tile.
+constexpr int kSortRows = kThreads;
+struct TileIds {
+    int row[32];                              // the tile's rows
+    alignas(16) uint32_t key[kSortRows];      // adapter * kSortRows + row
+};
+__device__ __forceinline__ void tile_rows(const AdapterArgs &g, int64_t first, int rows, int tiles, TileIds &s) {
+    const int i = int(threadIdx.x);
+    bool sorted = false;
+    if (g.tokens <= kSortRows && uint32_t(g.n_adapter) < 0xffffffffu / kSortRows) {
+        const int a = i < g.tokens ? adapter_of(g, i) : -1;
+        // rows without an adapter last
+        const uint32_t mine = uint32_t(a < 0 ? g.n_adapter : a) * kSortRows + uint32_t(i);
+        s.key[i] = i < g.tokens ? mine : 0xffffffffu;
+        __syncthreads();
+        sorted = __syncthreads_count(i > 0 && i < g.tokens && mine / kSortRows != s.key[i - 1] / kSortRows) > tiles;
+        if (sorted) {
+            int at = 0;
+#pragma unroll 4
+            for (int u = 0; u < g.tokens; u += 4) {
+                const u32x4 k = *reinterpret_cast<const u32x4 *>(s.key + u);
+                at += (k[0] < mine) + (k[1] < mine) + (k[2] < mine) + (k[3] < mine);
+            }
+            if (i < g.tokens && at >= first && at < first + rows) s.row[at - int(first)] = i;
+        }
+    }
+    if (!sorted && i < rows) s.row[i] = int(min(first + i, int64_t(g.tokens) - 1));
+    __syncthreads();
+}
+
+// The adapters of a tile's rows, the same in every wave: lane l has row l.
 struct TileRows {
     int id;               // this lane's row's adapter, -1: none (or no such row)
     uint64_t left;        // rows not handled yet
-    __device__ __forceinline__ TileRows(const AdapterArgs &g, int64_t first, int rows, int lane) {
-        id = lane < rows && first + lane < g.tokens ? adapter_of(g, first + lane) : -1;
+    __device__ __forceinline__ TileRows(const AdapterArgs &g, const TileIds &s, int count, int lane) {
+        id = lane < count ? adapter_of(g, s.row[lane]) : -1;
         left = __ballot(id >= 0);
+    }
+    // How many adapters the rows have.
+    __device__ __forceinline__ int distinct() const {
+        TileRows r = *this;
+        int n = 0;
+        while (r.next() >= 0) ++n;
+        return n;
     }
     // The next adapter of the tile, -1 at the end.
     __device__ __forceinline__ int next() {
@@ -252,13 +293,16 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterArgs g, A
     const int r0 = int(blockIdx.y) * 16 * NR;
     const int k0 = plane * s.slice + wave * 32 + (lane & 3) * 8;          // of a, as loaded
     const int k1 = min(g.n_in, (plane + 1) * s.slice);
-    TileRows rows(g, first, 16 * MR, lane);
+    __shared__ TileIds ids;
+    tile_rows(g, first, 16 * MR, s.tiles, ids);
+    const int count = int(min(int64_t(16 * MR), g.tokens - first));      // rows of the tile
+    TileRows rows(g, ids, count, lane);
     const int kx = plane * s.slice + wave * 32 + lane % kLanes * kRun;
     const T *x_at[kLoads];
 #pragma unroll
     for (int m = 0; m < kLoads; ++m)
         x_at[m] = static_cast<const T *>(g.x) +
-                  min(first + m * (64 / kLanes) + lane / kLanes, int64_t(g.tokens) - 1) * g.ldx;
+                  int64_t(ids.row[min(m * (64 / kLanes) + lane / kLanes, count - 1)]) * g.ldx;
     Turn &turn = lds.turn[wave];
     for (int pass = 0, a; (a = rows.next()) >= 0; ++pass) {
         if (pass % int(gridDim.z) != int(blockIdx.z)) continue;
@@ -346,9 +390,8 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterArgs g, A
             const f32x4 h = (lds.red[0][n][m][l] + lds.red[1][n][m][l]) +
                             (lds.red[2][n][m][l] + lds.red[3][n][m][l]);
             const int row = m * 16 + (l & 15), r = r0 + n * 16 + (l >> 4) * 4;
-            const int64_t t = first + row;
-            if (r < g.rank && t < g.tokens && adapter_of(g, t) == a)
-                *reinterpret_cast<f32x4 *>(g.ws + (int64_t(plane) * g.tokens + t) * g.rank + r) = h;
+            if (r < g.rank && row < count && adapter_of(g, ids.row[row]) == a)
+                *reinterpret_cast<f32x4 *>(g.ws + (int64_t(plane) * g.tokens + ids.row[row]) * g.rank + r) = h;
         }
         __syncthreads();
     }
@@ -383,7 +426,11 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterArgs g, Ada
     const int n_end = min(g.n_out, n_begin + per * kThreads);
     const T *base = static_cast<const T *>(g.base);
     T *out = static_cast<T *>(g.out);
-    TileRows rows(g, first, 16 * MR, lane);
+    __shared__ TileIds ids;
+    tile_rows(g, first, 16 * MR, s.tiles, ids);
+    const int count = int(min(int64_t(16 * MR), g.tokens - first));      // rows of the tile
+    TileRows rows(g, ids, count, lane);
+    if (blockIdx.z > 0 && int(blockIdx.z) >= rows.distinct()) return;      // no pass left for it
     // this lane's share of an access: its rows' adapters and its column
     const int col = wave * 64 + lane % kLanes * kRun;
     int id[MR][kParts];
@@ -394,7 +441,7 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterArgs g, Ada
         for (int i = 0; i < kParts; ++i) {
             const int r = m * 16 + i * kRows + lane / kLanes;
             id[m][i] = __shfl(rows.id, r);
-            row[m][i] = min(first + r, int64_t(g.tokens) - 1);
+            row[m][i] = ids.row[min(r, count - 1)];
         }
     Run b_run[MR][kParts];
     auto load_base = [&](int n) {
@@ -408,7 +455,7 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterArgs g, Ada
         for (int c = threadIdx.x; c < 16 * MR * (kUpRank / 4); c += kThreads) {
             const int r0 = c / (kUpRank / 4), r = b + c % (kUpRank / 4) * 4;
             if (r >= g.rank) continue;
-            const float *src = g.ws + min(first + r0, int64_t(g.tokens) - 1) * g.rank + r;
+            const float *src = g.ws + int64_t(ids.row[min(r0, count - 1)]) * g.rank + r;
             const int64_t plane = int64_t(g.tokens) * g.rank;
             f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
             for (int q = 0; q < s.splits; q += 4) {
@@ -430,7 +477,7 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterArgs g, Ada
     }
     // rows without an adapter
     const bool copied = blockIdx.z == 0 && g.out != g.base &&
-                        __popcll(rows.left) < min(int64_t(16 * MR), g.tokens - first);
+                        __popcll(rows.left) < count;
     if (copied)
         for (int n = n_begin + col; n < n_end; n += kThreads) {
             if (n > n_begin + col) load_base(n);
@@ -438,7 +485,7 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterArgs g, Ada
             for (int m = 0; m < MR; ++m)
 #pragma unroll
                 for (int i = 0; i < kParts; ++i)
-                    if (id[m][i] < 0 && first + m * 16 + i * kRows + lane / kLanes < g.tokens)
+                    if (id[m][i] < 0 && m * 16 + i * kRows + lane / kLanes < count)
                         stream_store(out + row[m][i] * g.ldo + n, b_run[m][i]);
         }
     for (int pass = 0, a; (a = rows.next()) >= 0; ++pass) {
@@ -575,9 +622,11 @@ hipError_t launch_adapters(const AdapterArgs &g, hipStream_t stream) {
         using One = std::integral_constant<int, 1>;
         using Two = std::integral_constant<int, 2>;
         using Four = std::integral_constant<int, 4>;
-        auto passes = [](int64_t groups) {
-            const int64_t n = 2048 / groups;
-            return unsigned(n < 1 ? 1 : n > 16 ? 16 : n);
+        // workgroups that share a tile's passes (one for each of its adapters):
+        // sorted rows need few, and each workgroup has to sort
+        auto passes = [&](int64_t groups) {
+            const int64_t most = g.tokens <= kSortRows ? 4 : 16, n = 2048 / groups;
+            return unsigned(n < 1 ? 1 : n > most ? most : n);
         };
         auto down = [&](auto NR, auto MR) {
             const unsigned blocks = unsigned((g.rank + 16 * NR.value - 1) / (16 * NR.value));

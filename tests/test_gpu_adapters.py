@@ -98,7 +98,8 @@ def ids_of(kind, T, n, seed=1):
 @pytest.mark.parametrize("T,n,rank,n_in,n_out", [
     (1, 1, 8, 8, 8), (1, 4, 16, 2560, 1280), (2, 3, 8, 64, 136), (15, 5, 24, 72, 64), (16, 2, 16, 256, 256),
     (17, 4, 64, 520, 264), (48, 32, 16, 2560, 128), (65, 3, 40, 96, 2560), (130, 7, 8, 1000, 72),
-    (200, 3, 128, 136, 200), (33, 2, 256, 40, 48)])
+    (200, 3, 128, 136, 200), (33, 2, 256, 40, 48), (130, 7, 64, 1000, 2056), (97, 40, 128, 72, 136),
+    (256, 3, 64, 264, 72), (250, 300, 56, 88, 96), (64, 2, 256, 40, 48), (129, 9, 104, 32, 1032)])
 @pytest.mark.parametrize("kind", ["one", "runs", "mixed", "wild", "none"])
 def test_adapters(T, n, rank, n_in, n_out, dtype, wdtype, kind):
     print("adapters", T, n, rank, n_in, n_out, dtype, wdtype, kind, flush=True)
@@ -118,11 +119,11 @@ def test_adapters(T, n, rank, n_in, n_out, dtype, wdtype, kind):
 
 
 @pytest.mark.parametrize("dtype,wdtype", TYPES)
-@pytest.mark.parametrize("T", [700, 1500, 4100])
-def test_many_rows(T, dtype, wdtype):
+@pytest.mark.parametrize("T,rank", [(257, 16), (700, 32), (1500, 64), (4100, 32), (4101, 8), (4200, 48), (4099, 72)])
+def test_many_rows(T, rank, dtype, wdtype):
     """Long batches, contiguous and shuffled: a row's result does not depend on its neighbours."""
-    n, rank, n_in, n_out = 5, 32, 264, 328
-    print("adapters, many rows", T, dtype, wdtype, flush=True)
+    n, n_in, n_out = 5, 264, 328
+    print("adapters, many rows", T, rank, dtype, wdtype, flush=True)
     ids = ids_of("runs", T, n, seed=T)
     d, want = make(T, n, rank, n_in, n_out, dtype, wdtype, ids, seed=3, pad=8)
     out = run(d, T)
