@@ -242,6 +242,10 @@ struct TileRows {
         id = lane < count ? adapter_of(g, s.row[lane]) : -1;
         left = __ballot(id >= 0);
     }
+    __device__ __forceinline__ TileRows(const AdapterArgs &g, int64_t first, int count, int lane) {
+        id = lane < count ? adapter_of(g, first + lane) : -1;
+        left = __ballot(id >= 0);
+    }
     // How many adapters the rows have.
     __device__ __forceinline__ int distinct() const {
         TileRows r = *this;
@@ -397,7 +401,7 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterArgs g, A
     }
 }
 
-// The update of a tile of 16 * MR rows, 256 outputs at a time (64 per wave).
+// The update of a tile of 16 rows, 256 outputs at a time (64 per wave).
 // h, its planes added, stands in LDS, all rows of the tile at once where the
 // rank fits (its loads then wait for nothing else); the matrix unit's rows are
 // outputs, its columns rows of the tile, and a pass's results are taken from
@@ -409,8 +413,9 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterArgs g, A
 constexpr int kUpRank = 64;          // rank values of h in LDS at a time
 constexpr int kUpStride = kUpRank + 4;
 
-template <int XT, int WT, int MR, int KB>
-__global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterArgs g, AdapterSplit s, int slices, int per) {
+template <int XT, int WT, int KB>
+__global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterArgs g, AdapterSplit s, int tiles, int slices,
+                                                              int per) {
     using T = typename Elem<XT>::T;
     constexpr int kHP = XT == kF32 ? 3 : 2;      // 16 bits of h are enough for 16-bit rows
     constexpr int kRun = XT == kF32 ? 4 : 8;     // 16 bytes of a row
@@ -418,41 +423,37 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterArgs g, Ada
     constexpr int kRows = 64 / kLanes;           // rows of one access
     constexpr int kParts = 16 / kRows;           // accesses of 16 rows
     struct alignas(16) Run { T e[kRun]; };
-    __shared__ float h[16 * MR][kUpStride];
+    __shared__ float h[16][kUpStride];
     __shared__ float turn[4][16][64 + 4];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t first = int64_t(blockIdx.x / slices) * (16 * MR);
+    const int64_t first = int64_t(blockIdx.x / slices) * 16;
     const int n_begin = int(blockIdx.x % slices) * per * kThreads;
     const int n_end = min(g.n_out, n_begin + per * kThreads);
     const T *base = static_cast<const T *>(g.base);
     T *out = static_cast<T *>(g.out);
     __shared__ TileIds ids;
-    tile_rows(g, first, 16 * MR, s.tiles, ids);
-    const int count = int(min(int64_t(16 * MR), g.tokens - first));      // rows of the tile
+    tile_rows(g, first, 16, tiles, ids);
+    const int count = int(min(int64_t(16), g.tokens - first));      // rows of the tile
     TileRows rows(g, ids, count, lane);
     if (blockIdx.z > 0 && int(blockIdx.z) >= rows.distinct()) return;      // no pass left for it
     // this lane's share of an access: its rows' adapters and its column
     const int col = wave * 64 + lane % kLanes * kRun;
-    int id[MR][kParts];
-    int64_t row[MR][kParts];
+    int id[kParts];
+    int64_t row[kParts];
 #pragma unroll
-    for (int m = 0; m < MR; ++m)
-#pragma unroll
-        for (int i = 0; i < kParts; ++i) {
-            const int r = m * 16 + i * kRows + lane / kLanes;
-            id[m][i] = __shfl(rows.id, r);
-            row[m][i] = ids.row[min(r, count - 1)];
-        }
-    Run b_run[MR][kParts];
+    for (int i = 0; i < kParts; ++i) {
+        const int r = i * kRows + lane / kLanes;
+        id[i] = __shfl(rows.id, r);
+        row[i] = ids.row[min(r, count - 1)];
+    }
+    Run b_run[kParts];
     auto load_base = [&](int n) {
 #pragma unroll
-        for (int m = 0; m < MR; ++m)
-#pragma unroll
-            for (int i = 0; i < kParts; ++i)
-                b_run[m][i] = stream_load<Run>(base + row[m][i] * g.ldb + min(n, g.n_out - kRun));
+        for (int i = 0; i < kParts; ++i)
+            b_run[i] = stream_load<Run>(base + row[i] * g.ldb + min(n, g.n_out - kRun));
     };
     auto stage = [&](int b) {
-        for (int c = threadIdx.x; c < 16 * MR * (kUpRank / 4); c += kThreads) {
+        for (int c = threadIdx.x; c < 16 * (kUpRank / 4); c += kThreads) {
             const int r0 = c / (kUpRank / 4), r = b + c % (kUpRank / 4) * 4;
             if (r >= g.rank) continue;
             const float *src = g.ws + int64_t(ids.row[min(r0, count - 1)]) * g.rank + r;
@@ -482,11 +483,9 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterArgs g, Ada
         for (int n = n_begin + col; n < n_end; n += kThreads) {
             if (n > n_begin + col) load_base(n);
 #pragma unroll
-            for (int m = 0; m < MR; ++m)
-#pragma unroll
-                for (int i = 0; i < kParts; ++i)
-                    if (id[m][i] < 0 && m * 16 + i * kRows + lane / kLanes < count)
-                        stream_store(out + row[m][i] * g.ldo + n, b_run[m][i]);
+            for (int i = 0; i < kParts; ++i)
+                if (id[i] < 0 && i * kRows + lane / kLanes < count)
+                    stream_store(out + row[i] * g.ldo + n, b_run[i]);
         }
     for (int pass = 0, a; (a = rows.next()) >= 0; ++pass) {
         if (pass % int(gridDim.z) != int(blockIdx.z)) continue;
@@ -509,25 +508,20 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterArgs g, Ada
         load_weights(n_begin);
         if (pass > 0 || copied) load_base(n_begin + col);
         for (int n0 = n_begin; n0 < n_end; n0 += kThreads) {
-            f32x4 acc[4][MR];
+            f32x4 acc[4];
 #pragma unroll
-            for (int m = 0; m < MR; ++m)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[j][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int j = 0; j < 4; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             auto multiply = [&](int b, int k, auto weight) {
-                u32x4 v[MR][kHP];
+                u32x4 v[kHP];
+                float f[8];
+                const float *src = &h[lane & 15][k - b + (lane >> 4) * 8];
+                *reinterpret_cast<f32x4 *>(f) = *reinterpret_cast<const f32x4 *>(src);
+                *reinterpret_cast<f32x4 *>(f + 4) = *reinterpret_cast<const f32x4 *>(src + 4);
+                // values past the rank may be anything, and 0 times that is not 0
+                if (k + 32 > rank)
 #pragma unroll
-                for (int m = 0; m < MR; ++m) {
-                    float f[8];
-                    const float *src = &h[m * 16 + (lane & 15)][k - b + (lane >> 4) * 8];
-                    *reinterpret_cast<f32x4 *>(f) = *reinterpret_cast<const f32x4 *>(src);
-                    *reinterpret_cast<f32x4 *>(f + 4) = *reinterpret_cast<const f32x4 *>(src + 4);
-                    // values past the rank may be anything, and 0 times that is not 0
-                    if (k + 32 > rank)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) f[i] = k + (lane >> 4) * 8 + i < rank ? f[i] : 0.0f;
-                    split<kHP>(f, v[m]);
-                }
+                    for (int i = 0; i < 8; ++i) f[i] = k + (lane >> 4) * 8 + i < rank ? f[i] : 0.0f;
+                split<kHP>(f, v);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     u32x4 raw = weight(j);
@@ -541,8 +535,7 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterArgs g, Ada
                     }
                     Weight<WT> w;
                     w.set(raw);
-#pragma unroll
-                    for (int m = 0; m < MR; ++m) acc[j][m] = mfma_parts(w.p, v[m], acc[j][m]);
+                    acc[j] = mfma_parts(w.p, v, acc[j]);
                 }
             };
             if constexpr (KB > 0) {
@@ -559,18 +552,170 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterArgs g, Ada
                         multiply(b, k, [&](int j) { return load_b(n0, j, k); });
                 }
             }
+            // results to rows: the wave's own part of LDS
+            __builtin_amdgcn_wave_barrier();
 #pragma unroll
-            for (int m = 0; m < MR; ++m) {
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<f32x4 *>(&turn[wave][lane & 15][j * 16 + (lane >> 4) * 4]) = acc[j];
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) {
+                const float *src = &turn[wave][i * kRows + lane / kLanes][lane % kLanes * kRun];
+                float u[kRun];
+#pragma unroll
+                for (int c = 0; c < kRun; c += 4)
+                    *reinterpret_cast<f32x4 *>(u + c) = *reinterpret_cast<const f32x4 *>(src + c);
+                Run r;
+#pragma unroll
+                for (int c = 0; c < kRun; ++c)
+                    r.e[c] = from_float<XT>(__builtin_fmaf(scale, u[c], to_float<XT>(b_run[i].e[c])));
+                if (id[i] == a && n0 + col < n_end) stream_store(out + row[i] * g.ldo + n0 + col, r);
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            if (n0 + kThreads < n_end) load_base(n0 + kThreads + col);
+        }
+    }
+}
+
+// The same for many rows and ranks up to 64: a workgroup takes 64 rows, a wave
+// 16 of them, and 64 outputs at a time.  The block of b is loaded once for the
+// four waves, in row order; h stays in registers, split, for all outputs.
+//   Bound by base and out: 16,384 fp32 rows of 2560 at rank 64 take 69 us (336
+// MB, 4.9 TB/s; the 16-row kernel 89, 32 rows of it 73).  Short stretches of
+// outputs are best, 1,024 / 2,048 / 4,096 / 10,240 workgroups 84 / 71 / 69 / 79
+// us.  2,047 fp16 rows at rank 24 take 12.9 us against the 16-row kernel's 10.6.
+constexpr int kWideGroups = 4096;
+
+template <int XT, int WT, int KB>
+__global__ __launch_bounds__(kThreads) void adapter_up_wide_kernel(AdapterArgs g, AdapterSplit s, int slices, int per) {
+    using T = typename Elem<XT>::T;
+    constexpr int kHP = XT == kF32 ? 3 : 2;
+    constexpr int kRun = XT == kF32 ? 4 : 8;     // 16 bytes of a row
+    constexpr int kLanes = 64 / kRun;            // lanes of a row's 64 outputs
+    constexpr int kRows = 64 / kLanes;           // rows of one access
+    constexpr int kParts = 16 / kRows;           // accesses of 16 rows
+    constexpr int kChunks = KB * 4;              // 16-byte runs of a row of b
+    struct alignas(16) Run { T e[kRun]; };
+    __shared__ uint16_t b_block[64][KB * 32 + 8];
+    __shared__ float turns[4][16][64 + 4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    auto &turn = turns[wave];
+    const int64_t first = int64_t(blockIdx.x / slices) * 64;
+    const int n_begin = int(blockIdx.x % slices) * per * 64;
+    const int n_end = min(g.n_out, n_begin + per * 64);
+    const T *base = static_cast<const T *>(g.base);
+    T *out = static_cast<T *>(g.out);
+    const int count = int(min(int64_t(64), g.tokens - first));
+    TileRows rows(g, first, count, lane);
+    if (blockIdx.z > 0 && int(blockIdx.z) >= rows.distinct()) return;      // no pass left for it
+    // this lane's share of an access: its rows' adapters and its column
+    const int col = lane % kLanes * kRun;
+    int id[kParts];
+    int64_t row[kParts];
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+        const int r = wave * 16 + i * kRows + lane / kLanes;
+        id[i] = __shfl(rows.id, r);
+        row[i] = first + min(r, count - 1);
+    }
+    Run b_run[kParts];
+    auto load_base = [&](int n) {
+#pragma unroll
+        for (int i = 0; i < kParts; ++i)
+            b_run[i] = stream_load<Run>(base + row[i] * g.ldb + min(n, g.n_out - kRun));
+    };
+    // h of the wave's rows, in the matrix unit's layout: row lane % 16, values
+    // (lane / 16) * 8 of each 32; zeros past the rank of the row's own adapter
+    u32x4 v[KB][kHP];
+    const int mine = __shfl(rows.id, wave * 16 + (lane & 15));
+    {
+        const int rank = mine >= 0 ? rank_of(g, mine) : 0;
+        const float *src = g.ws + (first + min(wave * 16 + (lane & 15), count - 1)) * g.rank;
+        const int64_t plane = int64_t(g.tokens) * g.rank;
+#pragma unroll
+        for (int q = 0; q < KB; ++q) {
+            const int k = q * 32 + (lane >> 4) * 8;
+            f32x4 f[2] = {};
+            for (int p = 0; p < s.splits; ++p)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    f[i] += *reinterpret_cast<const f32x4 *>(src + p * plane + min(k, g.rank - 8) + i * 4);
+            float e[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) e[j] = k + j < rank ? f[j / 4][j % 4] : 0.0f;
+            split<kHP>(e, v[q]);
+        }
+    }
+    load_base(n_begin + col);
+    // rows without an adapter
+    const bool copied = blockIdx.z == 0 && g.out != g.base && __popcll(rows.left) < count;
+    if (copied)
+        for (int n = n_begin + col; n < n_end; n += 64) {
+            if (n > n_begin + col) load_base(n);
+#pragma unroll
+            for (int i = 0; i < kParts; ++i)
+                if (id[i] < 0 && wave * 16 + i * kRows + lane / kLanes < count)
+                    stream_store(out + row[i] * g.ldo + n, b_run[i]);
+        }
+    for (int pass = 0, a; (a = rows.next()) >= 0; ++pass) {
+        if (pass % int(gridDim.z) != int(blockIdx.z)) continue;
+        const int rank = rank_of(g, a);
+        const float scale = g.scale[a];
+        const uint16_t *mat = static_cast<const uint16_t *>(g.b) + int64_t(a) * g.n_out * g.rank;
+        const bool here = __any(mine == a);      // this wave has rows of it
+        u32x4 w_run[KB];
+        auto load_block = [&](int n0) {
+#pragma unroll
+            for (int q = 0; q < KB; ++q) {
+                const int i = int(threadIdx.x) + q * kThreads;
+                w_run[q] = *reinterpret_cast<const u32x4 *>(mat + int64_t(min(n0 + i / kChunks, g.n_out - 1)) * g.rank +
+                                                            min(i % kChunks * 8, g.rank - 8));
+            }
+        };
+        auto store_block = [&] {
+#pragma unroll
+            for (int q = 0; q < KB; ++q) {
+                const int i = int(threadIdx.x) + q * kThreads, k = i % kChunks * 8;
+                u32x4 raw = w_run[q];
+                // columns past the adapter's rank are not part of it, whatever they hold
+                if (KB * 32 > rank)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        raw[j] = k + 2 * j + 1 < rank ? raw[j] : (k + 2 * j < rank ? raw[j] & 0xffffu : 0u);
+                *reinterpret_cast<u32x4 *>(&b_block[i / kChunks][k]) = raw;
+            }
+        };
+        load_block(n_begin);
+        if (pass > 0 || copied) load_base(n_begin + col);
+        store_block();
+        __syncthreads();
+        for (int n0 = n_begin; n0 < n_end; n0 += 64) {
+            const bool more = n0 + 64 < n_end;
+            if (more) load_block(n0 + 64);
+            if (here) {
+                f32x4 acc[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int q = 0; q < KB; ++q) {
+                        Weight<WT> w;
+                        w.set(*reinterpret_cast<const u32x4 *>(
+                            &b_block[j * 16 + (lane & 15)][q * 32 + (lane >> 4) * 8]));
+                        acc[j] = mfma_parts(w.p, v[q], acc[j]);
+                    }
+                }
                 // results to rows: the wave's own part of LDS
                 __builtin_amdgcn_wave_barrier();
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    *reinterpret_cast<f32x4 *>(&turn[wave][lane & 15][j * 16 + (lane >> 4) * 4]) = acc[j][m];
+                    *reinterpret_cast<f32x4 *>(&turn[lane & 15][j * 16 + (lane >> 4) * 4]) = acc[j];
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
                 __builtin_amdgcn_wave_barrier();
 #pragma unroll
                 for (int i = 0; i < kParts; ++i) {
-                    const float *src = &turn[wave][i * kRows + lane / kLanes][lane % kLanes * kRun];
+                    const float *src = &turn[i * kRows + lane / kLanes][col];
                     float u[kRun];
 #pragma unroll
                     for (int c = 0; c < kRun; c += 4)
@@ -578,12 +723,17 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterArgs g, Ada
                     Run r;
 #pragma unroll
                     for (int c = 0; c < kRun; ++c)
-                        r.e[c] = from_float<XT>(__builtin_fmaf(scale, u[c], to_float<XT>(b_run[m][i].e[c])));
-                    if (id[m][i] == a && n0 + col < n_end) stream_store(out + row[m][i] * g.ldo + n0 + col, r);
+                        r.e[c] = from_float<XT>(__builtin_fmaf(scale, u[c], to_float<XT>(b_run[i].e[c])));
+                    if (id[i] == a && n0 + col < n_end) stream_store(out + row[i] * g.ldo + n0 + col, r);
                 }
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                if (more) load_base(n0 + 64 + col);
             }
-            if (n0 + kThreads < n_end) load_base(n0 + kThreads + col);
+            __syncthreads();
+            if (more) {
+                store_block();
+                __syncthreads();
+            }
         }
     }
 }
@@ -634,31 +784,39 @@ hipError_t launch_adapters(const AdapterArgs &g, hipStream_t stream) {
             hipLaunchKernelGGL((adapter_down_kernel<XT.value, WT.value, NR.value, MR.value>), grid, dim3(kThreads),
                                0, stream, g, s);
         };
-        auto up = [&](auto MR) {
-            const int all = (g.n_out + kThreads - 1) / kThreads;
-            int slices = int((2048 + int64_t(s.tiles) - 1) / s.tiles);
+        auto up_wide = [&](auto KB) {
+            const int tiles = (g.tokens + 63) / 64, all = (g.n_out + 63) / 64;
+            int slices = (kWideGroups + tiles - 1) / tiles;
             if (slices > all) slices = all;
             const int per = all / slices;               // rounded down: even shares, some more workgroups
             slices = (all + per - 1) / per;
-            const dim3 grid(unsigned(s.tiles) * unsigned(slices), 1, passes(int64_t(s.tiles) * slices));
-            auto go = [&](auto KB) {
-                hipLaunchKernelGGL((adapter_up_kernel<XT.value, WT.value, MR.value, KB.value>), grid,
-                                   dim3(kThreads), 0, stream, g, s, slices, per);
-            };
-            if (g.rank <= 32) go(One{});
-            else if (g.rank <= 64) go(Two{});
-            else go(std::integral_constant<int, 0>{});
+            const dim3 grid(unsigned(tiles) * unsigned(slices), 1, passes(int64_t(tiles) * slices));
+            hipLaunchKernelGGL((adapter_up_wide_kernel<XT.value, WT.value, KB.value>), grid, dim3(kThreads), 0, stream,
+                               g, s, slices, per);
         };
-        auto both = [&](auto MR) {
+        auto up = [&](auto KB) {
+            const int tiles = (g.tokens + 15) / 16, all = (g.n_out + kThreads - 1) / kThreads;
+            int slices = (2048 + tiles - 1) / tiles;
+            if (slices > all) slices = all;
+            const int per = all / slices;
+            slices = (all + per - 1) / per;
+            const dim3 grid(unsigned(tiles) * unsigned(slices), 1, passes(int64_t(tiles) * slices));
+            hipLaunchKernelGGL((adapter_up_kernel<XT.value, WT.value, KB.value>), grid, dim3(kThreads), 0, stream, g, s,
+                               tiles, slices, per);
+        };
+        auto by_rank = [&](auto MR) {
             if (g.rank <= 16) down(One{}, MR);
             else if (g.rank <= 32) down(Two{}, MR);
             else down(Four{}, MR);
-            const hipError_t err = hipGetLastError();
-            if (err != hipSuccess) return err;
-            up(MR);
             return hipGetLastError();
         };
-        return s.row_groups == 1 ? both(One{}) : both(Two{});
+        const hipError_t err = s.row_groups == 1 ? by_rank(One{}) : by_rank(Two{});
+        if (err != hipSuccess) return err;
+        const bool wide = g.tokens > kAdapterLongRows;
+        if (g.rank > 64) up(std::integral_constant<int, 0>{});
+        else if (g.rank > 32) wide ? up_wide(Two{}) : up(Two{});
+        else wide ? up_wide(One{}) : up(One{});
+        return hipGetLastError();
     });
 }
 

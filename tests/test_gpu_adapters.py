@@ -119,7 +119,7 @@ def test_adapters(T, n, rank, n_in, n_out, dtype, wdtype, kind):
 
 
 @pytest.mark.parametrize("dtype,wdtype", TYPES)
-@pytest.mark.parametrize("T,rank", [(257, 16), (700, 32), (1500, 64), (4100, 32), (4101, 8), (4200, 48), (4099, 72)])
+@pytest.mark.parametrize("T,rank", [(257, 16), (700, 32), (1500, 64), (4100, 32), (4101, 8), (8193, 8), (8200, 48), (8250, 72)])
 def test_many_rows(T, rank, dtype, wdtype):
     """Long batches, contiguous and shuffled: a row's result does not depend on its neighbours."""
     n, n_in, n_out = 5, 264, 328
