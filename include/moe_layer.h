@@ -109,8 +109,9 @@ int moe_route_backward(const void *logits, int64_t ld, int dtype, int tokens, in
  * dm, ddm: device fp32 [tokens*topk x hidden]; w, dw: device fp32
  * [tokens x topk]; dout: device fp32 [tokens x hidden]; hidden % 4 == 0
  * (MOE_EFORMAT).  dw or ddm may be NULL (not both): without dw, dm may be
- * NULL; without ddm, w may be.  No plan is needed, so the backward pass of a
- * layer may run after its plan is gone. */
+ * NULL; without ddm, w may be.  MOE_EINVAL if tokens * topk exceeds 2^30 or
+ * tokens * ceil(topk / 8) reaches 2^26 (the launch's thread count).  No plan
+ * is needed, so the backward pass of a layer may run after its plan is gone. */
 int moe_combine_backward(const float *dm, const float *w, const float *dout, int tokens, int topk,
                          int hidden, float *dw, float *ddm, void *stream);
 
@@ -155,7 +156,9 @@ size_t moe_adapters_bytes(const moe_adapter_set *set, int tokens);
  *          it shares none with x
  *   workspace  device, moe_adapters_bytes(set, tokens) bytes, 16-byte
  *          aligned, free again when the call's work has run
- * a * x is held in fp32, the result rounded once. */
+ * a * x is held in fp32, the result rounded once.  What a row holds reaches no
+ * other row; an infinity in fp32 x may give NaN where the formula has an
+ * infinity.  A row's result does not depend on the rows beside it. */
 int moe_adapters(const moe_adapter_set *set, const int32_t *ids, int tokens, int dtype,
                  const void *x, int64_t ldx, const void *base, int64_t ldb, void *out, int64_t ldo,
                  void *workspace, size_t workspace_bytes, void *stream);

@@ -324,3 +324,45 @@ def test_binding_refusals():
     assert status(moe.moe_adapters, s, i, x, y, y, ws[:-16]) == -4
     assert status(moe.AdapterSet, a, torch.zeros(2, 32, 8, device="cuda", dtype=torch.bfloat16),
                   torch.ones(2, device="cuda")) == -1
+
+
+def test_no_tokens():
+    """Empty batches through the binding: accepted, the statistics written as zeros."""
+    e = lambda *shape, dtype=torch.float32: torch.empty(*shape, dtype=dtype, device="cuda")
+    l, ids, w = e(0, 60), e(0, 6, dtype=torch.int32), e(0, 6)
+    moe.moe_route(l, ids, w)
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    counts, probs, loss = torch.ones(2, 60, dtype=torch.int32, device="cuda"), e(2, 60).fill_(1), e(1).fill_(1)
+    ws = e(moe.moe_balance_bytes(0, 60, 2), dtype=torch.uint8)
+    moe.moe_route_balance(l, off, 0.1, ids, w, counts, probs, loss, ws)
+    assert not counts.any() and not probs.any() and not loss.any()
+    moe.moe_route_backward(l, ids, w, e(0, 60), seq_off=off, coef=0.1, counts=counts)
+    moe.moe_combine_backward(e(0, 64), w, e(0, 64), e(0, 6), e(0, 64))
+    s = moe.AdapterSet(e(2, 8, 64, dtype=torch.bfloat16), e(2, 32, 8, dtype=torch.bfloat16), e(2))
+    moe.moe_adapters(s, e(0, dtype=torch.int32), e(0, 64), e(0, 32), e(0, 32), e(16, dtype=torch.uint8))
+    torch.cuda.synchronize()
+
+
+def test_many_sequences():
+    """As many sequences as tokens and thousands more, empty: every one is written."""
+    T, E, K, S = 300, 40, 3, 9000
+    dev, l = make(T, E, "f32", seed=8)
+    rng = np.random.default_rng(1)
+    off = np.sort(np.concatenate([[0], rng.integers(0, T + 1, S - 1), [T]]))
+    o = [torch.empty(T, K, dtype=torch.int32, device="cuda"), torch.empty(T, K, device="cuda"),
+         torch.full((S, E), -1, dtype=torch.int32, device="cuda"), torch.full((S, E), -1.0, device="cuda"),
+         torch.empty(1, device="cuda")]
+    ws = torch.full((moe.moe_balance_bytes(T, E, S),), 0xFF, dtype=torch.uint8, device="cuda")
+    moe.moe_route_balance(dev, torch.from_numpy(off.astype(np.int32)).cuda(), 0.3, *o, ws)
+    want_c, want_p, want_l = ref.balance(l, ref.choice(l, K), off, 0.3)
+    assert np.array_equal(o[2].cpu().numpy(), want_c)
+    assert np.all(np.abs(o[3].cpu().numpy() - want_p) <= want_p * (rtol(E) + 40 * ref.U) + 0.5 * ref.U)
+    # the probabilities' 0.5 u enter times coef / S * E / (K n) * K n per filled sequence
+    filled = np.count_nonzero(np.diff(off))
+    assert abs(float(o[4]) - want_l) <= want_l * (rtol(E) + 64 * ref.U) + 0.3 / S * filled * E * 0.5 * ref.U
+    # and the gradient, with every token in a sequence of its own length
+    d = torch.empty(T, E, device="cuda")
+    moe.moe_route_backward(dev, o[0], None, d, seq_off=torch.from_numpy(off.astype(np.int32)).cuda(), coef=0.3,
+                           counts=o[2])
+    want, size = ref.route_backward(l, ref.choice(l, K), None, True, 1.0, off, 0.3, want_c)
+    assert np.all(np.abs(d.cpu().numpy() - want) <= size * (rtol(E, 16.0) + 32 * ref.U) + 1e-38)

@@ -138,7 +138,8 @@ def combine(**kw):
 
 @pytest.mark.parametrize("kw,want", [
     (dict(tokens=-1), EINVAL), (dict(topk=0), EINVAL), (dict(hidden=0), EINVAL), (dict(hidden=66), EFORMAT),
-    (dict(tokens=1 << 30, topk=2), EINVAL), (dict(dout=None), EINVAL), (dict(dw=None, ddm=None), EINVAL),
+    (dict(tokens=1 << 30, topk=2), EINVAL), (dict(tokens=1 << 26, topk=8), EINVAL),
+    (dict(tokens=1 << 25, topk=9), EINVAL), (dict(dout=None), EINVAL), (dict(dw=None, ddm=None), EINVAL),
     (dict(dm=None), EINVAL), (dict(w=None), EINVAL)]
     + [({k: P + OFF}, EALIGN) for k in ("dm", "w", "dout", "dw", "ddm")])
 def test_combine_backward_refusals(kw, want):
