@@ -70,10 +70,10 @@ def _load_torch():
 
 def _current(stream, t, what: str):
     """The current device, which has to hold t, and the raw stream (torch's current one by
-    default).  A call is a few microseconds, most of them this module's: hence raw handles and
+    default).  A call is a few microseconds, half of them this module's: hence raw handles and
     few calls per tensor."""
     c = _load_torch()._C
-    device = t.get_device() if t is not None and t.is_cuda else -1
+    device = -1 if t is None else t.get_device()
     if device < 0 or device != c._cuda_getDevice():
         raise MoeError(-1, f"{what}: {'None' if t is None else t.device} is not the current device")
     if stream is None:
@@ -88,33 +88,30 @@ def _dtype(t, what: str) -> int:
     return code
 
 
-def _place(device: int, t, what: str):
-    """The address of a tensor on the current device."""
-    if t.get_device() != device or device < 0:
-        raise MoeError(-1, f"{what}: on {t.device}, the current device is cuda:{device}")
-    return t.data_ptr()
-
-
 def _dense(device: int, t, what: str, dtype, shape):
-    """The address of a dense tensor of the given type and shape (None: no tensor)."""
+    """The address of a dense tensor of the given type, shape and device (None: no tensor)."""
     if t is None:
         return None
-    if t.dtype != dtype:
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device >= 0:
+        return t.data_ptr()
+    if t.dtype is not dtype:
         raise MoeError(-3, f"{what}: {t.dtype} instead of {dtype}")
     if t.shape != shape or not t.is_contiguous():
         raise MoeError(-1, f"{what}: shape {tuple(t.shape)}, strides {t.stride()}; dense {tuple(shape)} wanted")
-    if t.get_device() == device and device >= 0:
-        return t.data_ptr()
-    return _place(device, t, what)
+    raise MoeError(-1, f"{what}: on {t.device}, the current device is cuda:{device}")
 
 
 def _rows(device: int, t, what: str, shape, written: bool = False):
     """The address and row stride of a matrix with dense rows (that do not overlap, if written)."""
-    ld, step = t.stride() if t.dim() == 2 else (0, 0)
-    if t.shape != shape or (step != 1 and shape[1] > 1) or (written and ld < shape[1] and shape[0] > 1):
-        raise MoeError(-1, f"{what}: shape {tuple(t.shape)}, strides {t.stride()}; {tuple(shape)} with dense rows wanted")
+    if t.shape != shape:
+        raise MoeError(-1, f"{what}: shape {tuple(t.shape)}; {tuple(shape)} wanted")
+    ld, step = t.stride()
+    if (step != 1 and shape[1] > 1) or (written and ld < shape[1] and shape[0] > 1):
+        raise MoeError(-1, f"{what}: strides {t.stride()}; dense rows wanted")
+    if t.get_device() != device:
+        raise MoeError(-1, f"{what}: on {t.device}, the current device is cuda:{device}")
     # the stride of a single row says nothing: torch may give it any value
-    return _place(device, t, what), ld if shape[0] > 1 else shape[1]
+    return t.data_ptr(), ld if shape[0] > 1 else shape[1]
 
 
 def _matrix(t, what: str):
@@ -124,8 +121,9 @@ def _matrix(t, what: str):
 
 
 def _route(device: int, logits, topk: int, renorm: bool, scale: float):
-    T, E = _matrix(logits, "logits")
-    ptr, ld = _rows(device, logits, "logits", (T, E))
+    shape = _matrix(logits, "logits")
+    ptr, ld = _rows(device, logits, "logits", shape)
+    T, E = shape
     return (ptr, ld, _dtype(logits, "logits"), T, E, topk, MOE_ROUTE_RENORM if renorm else 0, scale)
 
 
@@ -168,7 +166,9 @@ def moe_route_balance(logits, seq_off, coef: float, ids, w, counts, probs, loss,
 def _workspace(device: int, t):
     if not t.is_contiguous():
         raise MoeError(-1, f"workspace: strides {t.stride()}")
-    return _place(device, t, "workspace"), t.numel() * t.element_size()
+    if t.get_device() != device:
+        raise MoeError(-1, f"workspace: on {t.device}, the current device is cuda:{device}")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def moe_route_backward(logits, ids, dw, dlogits, renorm: bool = True, scale: float = 1.0, seq_off=None,
