@@ -164,6 +164,8 @@ def moe_route_balance(logits, seq_off, coef: float, ids, w, counts, probs, loss,
 
 
 def _workspace(device: int, t):
+    if t is None:
+        return None, 0
     if not t.is_contiguous():
         raise MoeError(-1, f"workspace: strides {t.stride()}")
     if t.get_device() != device:

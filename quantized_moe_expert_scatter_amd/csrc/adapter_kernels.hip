@@ -4,7 +4,7 @@
 // Few rows take one launch: a workgroup has one row and a slice of its
 // outputs, and computes the row's low-rank values h = a[i] * x[t] itself.
 // More rows take two: the rows' h (fp32, in the workspace), then the update of
-// the output rows.
+// the output rows, by tiles of 16 rows, or of 64 in long batches.
 #include "layer_ops.h"
 #include "wave.cuh"
 
@@ -19,9 +19,10 @@ namespace {
 constexpr int kThreads = 256;
 // The single launch computes a row's h in each of its output slices, so it is
 // taken while tokens * rank * slices is small.  Measured at 2560 -> 2560 (3
-// slices) against the two launches, rows of one adapter / every row its own:
-// rank 16, 128 rows 7.0 / 8.3 us against 9.7 / 21.7; rank 64, 64 rows 11.3 /
-// 16.0 against 12.0 / 20; 128 rows 20.5 / 29.0 against 12.1 / 27.5.
+// slices), rows of one adapter / every row its own: rank 16, 256 rows 9.4 /
+// 12.4 us in one launch, 257 rows 8.5 / 35 in two; rank 32, 128 rows 10.1 /
+// 14.2 in one, 200 rows 9.9 / 20.4 in two; rank 64, 64 rows 11.3 / 16.9 in one,
+// 128 rows 20.5 / 29.0 in one and 10.9 / 21.4 in two.
 constexpr int kFewRows = 256;
 constexpr int kFewValues = 12288;
 
@@ -63,7 +64,9 @@ constexpr int kRowWaves = kRowThreads / 64;
 
 // One workgroup per (row, 1024 outputs).  h: each wave takes every 16th rank
 // row, RW of them at most, and passes over the row of x once; the outputs:
-// one per thread, its row of b (16-byte runs) against h from LDS.
+// one per thread, its row of b (16-byte runs) against h from LDS.  Latency: one
+// row of 2560 -> 2560 takes 4.4 us at rank 16, 10.4 at rank 64; 48 rows of 32
+// adapters, rank 16, 1280 outputs, 5.1.
 template <int XT, int WT, int RW>
 __global__ __launch_bounds__(kRowThreads) void adapter_row_kernel(AdapterArgs g, int slices) {
     using T = typename Elem<XT>::T;
@@ -401,15 +404,18 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterArgs g, A
     }
 }
 
-// The update of a tile of 16 rows, 256 outputs at a time (64 per wave).
-// h, its planes added, stands in LDS, all rows of the tile at once where the
-// rank fits (its loads then wait for nothing else); the matrix unit's rows are
-// outputs, its columns rows of the tile, and a pass's results are taken from
-// the columns whose rows have its adapter.  The 16 x 64 results pass through LDS so that base
-// and out move in whole row segments: 256 bytes of a row per 16 lanes reach
-// 6.2 TB/s in a copy of this shape, the 64 that the matrix unit's layout gives
-// 4.6.  KB: blocks of 32 rank values whose part of b is held in registers and
-// loaded while h is staged (0: any rank, 64 values at a time).
+// The update of a tile of 16 rows, 256 outputs at a time (64 per wave).  h, its
+// planes added, stands in LDS, all rows of the tile at once where the rank fits
+// (its loads then wait for nothing else); the matrix unit's rows are outputs,
+// its columns rows of the tile, and a pass's results are taken from the columns
+// whose rows have its adapter.  The 16 x 64 results pass through LDS so that
+// base and out move in whole row segments: 256 bytes of a row per 16 lanes
+// reach 6.2 TB/s in a copy of this shape, the 64 that the matrix unit's layout
+// gives 4.6.  KB: blocks of 32 rank values whose part of b is held in registers
+// (0: any rank, 64 values at a time).
+//   2,047 fp16 rows of 2560 at rank 24: 10.5 us for 21 MB.  Loading the first
+// part of b with base and h, or all planes of h at once, was slower (11.6-12.3),
+// b turned through LDS as in the other kernel level (11.1).
 constexpr int kUpRank = 64;          // rank values of h in LDS at a time
 constexpr int kUpStride = kUpRank + 4;
 
@@ -423,8 +429,8 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterArgs g, Ada
     constexpr int kRows = 64 / kLanes;           // rows of one access
     constexpr int kParts = 16 / kRows;           // accesses of 16 rows
     struct alignas(16) Run { T e[kRun]; };
-    __shared__ float h[16][kUpStride];
-    __shared__ float turn[4][16][64 + 4];
+    __shared__ alignas(16) float h[16][kUpStride];
+    __shared__ alignas(16) float turn[4][16][64 + 4];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t first = int64_t(blockIdx.x / slices) * 16;
     const int n_begin = int(blockIdx.x % slices) * per * kThreads;
@@ -597,8 +603,8 @@ __global__ __launch_bounds__(kThreads) void adapter_up_wide_kernel(AdapterArgs g
     constexpr int kParts = 16 / kRows;           // accesses of 16 rows
     constexpr int kChunks = KB * 4;              // 16-byte runs of a row of b
     struct alignas(16) Run { T e[kRun]; };
-    __shared__ uint16_t b_block[64][KB * 32 + 8];
-    __shared__ float turns[4][16][64 + 4];
+    __shared__ alignas(16) uint16_t b_block[64][KB * 32 + 8];
+    __shared__ alignas(16) float turns[4][16][64 + 4];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     auto &turn = turns[wave];
     const int64_t first = int64_t(blockIdx.x / slices) * 64;

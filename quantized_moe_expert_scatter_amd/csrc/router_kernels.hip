@@ -153,8 +153,8 @@ __device__ __forceinline__ void sort_keys(uint32_t (&k)[N]) {
 // the `times` rounds just before had the same lane and key (equal keys leave a
 // lane one after the other, as the first lane that has the largest key is
 // always the one taken).
-//   The kernel is bound by these operations (424 a row before the last three
-// of the steps above, 11 us at 16,384 rows of 512 on all vector units).
+//   The router is bound by these operations: 16,384 fp32 rows of 512, top-10,
+// take 11 us (35 MB, 3.2 TB/s), top-1 7.
 template <int J> struct Lists {
     // the last two: the 0, and what a lane taken J times reads
     uint32_t place[J + 2][kPlaceStride<J>];
@@ -323,7 +323,10 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
 
 // One workgroup per range of tokens: routes them and sums each sequence's part
 // of the range, p in registers (then over the waves through LDS), the choices
-// in an LDS histogram.
+// in an LDS histogram.  16,384 fp32 rows of 512: 15.5 us, the routing's 11 and
+// the exponentials of whole rows.  (At 1,024 threads two workgroups share a CU
+// only while a wave takes no more than about 80 scalar registers: lane masks
+// for each of the J places cost 5 us here.)
 template <int J, int DT, bool VEC>
 __global__ __launch_bounds__(64 * balance_waves(J)) void route_balance_kernel(RouteArgs a, BalanceLayout L) {
     constexpr int kWaves = balance_waves(J), kThreads = 64 * kWaves;
@@ -462,7 +465,8 @@ __global__ __launch_bounds__(64 * kJoinWaves) void balance_join_kernel(RouteArgs
 // The gradient of one token's row.  The chosen experts' parts are scattered
 // through the wave's LDS: each chosen id first writes its lane's number and
 // reads it back, and only if an id is named twice (never by moe_route) are the
-// parts added one after the other.
+// parts added one after the other.  16,384 fp32 rows of 512: 17 us (68 MB, 4.0
+// TB/s; 30 with a search through the registers for each choice).
 template <int J, int DT, bool VEC>
 __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteArgs a) {
     using T = typename Elem<DT>::T;

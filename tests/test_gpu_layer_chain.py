@@ -148,6 +148,49 @@ def test_captured_and_replayed():
     assert G.check_guards() == []
 
 
+@pytest.mark.parametrize("T,rank,dtype", [(300, 24, torch.float32), (300, 72, torch.bfloat16), (8200, 48, torch.float32)])
+def test_long_batches_captured(T, rank, dtype):
+    """The adapters' two-launch forms and the combine's gradient with the rows', replayed over changed inputs."""
+    H = 256
+    g = torch.Generator().manual_seed(T)
+    a, b = torch.randn(5, rank, H, generator=g).bfloat16().cuda(), torch.randn(5, H, rank, generator=g).bfloat16().cuda()
+    s = moe.AdapterSet(a, b, torch.rand(5, generator=g).cuda())
+    ids = torch.empty(T, dtype=torch.int32, device="cuda")
+    x, base, out = (torch.empty(T, H, dtype=dtype, device="cuda") for _ in range(3))
+    ws = torch.empty(moe.moe_adapters_bytes(s, T), dtype=torch.uint8, device="cuda")
+    dm, w, dout = torch.empty(T * 3, H, device="cuda"), torch.empty(T, 3, device="cuda"), torch.empty(T, H, device="cuda")
+    dw, ddm = torch.empty(T, 3, device="cuda"), torch.empty(T * 3, H, device="cuda")
+
+    def step(o, d, dd):
+        moe.moe_adapters(s, ids, x, base, o, ws)
+        moe.moe_combine_backward(dm, w, dout, d, dd)
+
+    def fill(seed):
+        h = torch.Generator().manual_seed(seed)
+        ids.copy_(torch.randint(-1, 5, (T // 7 + 1,), generator=h, dtype=torch.int32).repeat_interleave(7)[:T])
+        for t in (x, base, dm, w, dout):
+            t.copy_(torch.randn(t.shape, generator=h))
+
+    fill(0)
+    step(out, dw, ddm)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(out, dw, ddm)
+    for seed in (1, 2, 3):
+        fill(seed)
+        eager = [torch.empty_like(t) for t in (out, dw, ddm)]
+        step(*eager)
+        torch.cuda.synchronize()
+        ws.fill_(0xFF)
+        for t in (out, dw, ddm):
+            t.fill_(0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, want in zip((out, dw, ddm), eager):
+            assert torch.equal(got, want)
+
+
 def test_two_at_once():
     """Two calls of each kind on two streams, with workspaces of their own, over the same inputs and
     matrices: each gives what it gives alone."""
