@@ -273,19 +273,17 @@ __device__ __forceinline__ int sequence_of(const int32_t *seq_off, int n_seq, in
     return lo;
 }
 
-// Routes token t; with STATS the row's softmax is added to acc.
+// Routes token t.  With STATS it returns the row's softmax, v * inv, and lane
+// k's choice.
 template <int J, int DT, bool VEC, bool STATS>
-__device__ __forceinline__ void route_token(const RouteArgs &a, int t, int lane, bool count,
-                                            float (&acc)[J], int *hist, Lists<J> &lists) {
-    float v[J];
+__device__ __forceinline__ void route_token(const RouteArgs &a, int t, int lane, float (&v)[J], float &inv,
+                                            int &id, float &logit, Lists<J> &lists) {
     load_row<J, DT, VEC>(a.logits, int64_t(t) * a.ld, a.n_expert, lane, v, &lists.place[0][0]);
-    int id;
-    float logit;
     const float top = choose<J, DT, VEC>(a, int64_t(t) * a.ld, v, lane, id, logit, lists);
     const float shift = softmax_shift(top);
     const bool chosen = lane < a.topk;
     const float e = chosen ? exp_neg(logit - shift) : 0.0f;
-    float inv = 0.0f;
+    inv = 0.0f;
     if (STATS || !a.renorm) {
         float part = 0.0f;
 #pragma unroll
@@ -295,19 +293,15 @@ __device__ __forceinline__ void route_token(const RouteArgs &a, int t, int lane,
         }
         const float sum = wave_sum(part);
         inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        if (STATS && count) {
-#pragma unroll
-            for (int j = 0; j < J; ++j) acc[j] = __builtin_fmaf(v[j], inv, acc[j]);
-        }
     }
+    float w = inv;
     if (a.renorm) {
         const float sum = wave_sum(e);
-        inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        w = sum == 0.0f ? 0.0f : 1.0f / sum;
     }
     if (chosen) {
         a.ids[int64_t(t) * a.topk + lane] = id;
-        a.w[int64_t(t) * a.topk + lane] = a.scale * (e * inv);
-        if (STATS && count && logit != -INFINITY) atomicAdd(hist + id, 1);
+        a.w[int64_t(t) * a.topk + lane] = a.scale * (e * w);
     }
 }
 
@@ -315,20 +309,26 @@ template <int J, int DT, bool VEC>
 __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
     const int lane = threadIdx.x & 63;
     __shared__ Lists<J> lists[kRouteWaves];
-    float none[J];
     for (int64_t t = int64_t(blockIdx.x) * kRouteWaves + (threadIdx.x >> 6); t < a.tokens;
-         t += int64_t(gridDim.x) * kRouteWaves)
-        route_token<J, DT, VEC, false>(a, int(t), lane, false, none, nullptr, lists[threadIdx.x >> 6]);
+         t += int64_t(gridDim.x) * kRouteWaves) {
+        float v[J], inv, logit;
+        int id;
+        route_token<J, DT, VEC, false>(a, int(t), lane, v, inv, id, logit, lists[threadIdx.x >> 6]);
+    }
 }
 
-// One workgroup per range of tokens: routes them and sums each sequence's part
-// of the range, p in registers (then over the waves through LDS), the choices
-// in an LDS histogram.  16,384 fp32 rows of 512: 15.5 us, the routing's 11 and
-// the exponentials of whole rows.  (At 1,024 threads two workgroups share a CU
-// only while a wave takes no more than about 80 scalar registers: lane masks
-// for each of the J places cost 5 us here.)
+// One workgroup per range of tokens: its waves route a token each and then add
+// what they have to the sums of the token's sequence, p in registers (over the
+// waves through LDS where a sequence ends), the choices in an LDS histogram.
+// Several sequences in one round cost their sums only: 12 tokens in 8 sequences
+// take 18 us with the joining kernel, 30 with a round for each.
+//   16,384 fp32 rows of 512: 15.5 us, the routing's 11 and the exponentials of
+// whole rows.  Two workgroups of 1,024 threads share a CU only while a wave
+// keeps to 64 vector and about 80 scalar registers; left alone the compiler
+// holds a lane mask for each of the J places in the latter (5 us here).
 template <int J, int DT, bool VEC>
-__global__ __launch_bounds__(64 * balance_waves(J)) void route_balance_kernel(RouteArgs a, BalanceLayout L) {
+__global__ __attribute__((amdgpu_waves_per_eu(J <= 8 ? 8 : 1))) __launch_bounds__(64 * balance_waves(J)) void
+route_balance_kernel(RouteArgs a, BalanceLayout L) {
     constexpr int kWaves = balance_waves(J), kThreads = 64 * kWaves;
     __shared__ Lists<J> lists[kWaves];        // while routing; then the waves' sums, from place[0] on
     __shared__ int hist[64 * J];
@@ -343,41 +343,55 @@ __global__ __launch_bounds__(64 * balance_waves(J)) void route_balance_kernel(Ro
     float acc[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) acc[j] = 0.0f;
-    for (int pos = t0; pos < t1;) {
-        const int s = sequence_of(a.seq_off, a.n_seq, pos, lane);
-        int end = t1;
-        bool inside = s < a.n_seq;
-        if (inside) {
-            const int b = a.seq_off[s], e = a.seq_off[s + 1];
-            if (pos < b) {              // in front of the first sequence
-                inside = false;
-                end = min(b, t1);
-            } else if (e > pos) {
-                end = min(e, t1);
+    int s = 0, end = t0;                       // the sequence at hand ends (or leaves the range) there
+    bool inside = false;
+    for (int round = t0; round < t1; round += kWaves) {
+        const int t = round + wave, round_end = t1 - round < kWaves ? t1 : round + kWaves;
+        float v[J], inv = 0.0f, logit = -INFINITY;
+        int id = 0;
+        if (t < round_end) route_token<J, DT, VEC, true>(a, t, lane, v, inv, id, logit, lists[wave]);
+        for (int pos = round; pos < round_end;) {
+            if (pos >= end) {
+                s = sequence_of(a.seq_off, a.n_seq, pos, lane);
+                inside = s < a.n_seq;
+                end = t1;
+                if (inside) {
+                    const int b = a.seq_off[s], e = a.seq_off[s + 1];
+                    if (pos < b) {              // in front of the first sequence
+                        inside = false;
+                        end = min(b, t1);
+                    } else if (e > pos) {
+                        end = min(e, t1);
+                    }
+                }
             }
-        }
-        for (int t = pos + wave; t < end; t += kWaves)
-            route_token<J, DT, VEC, true>(a, t, lane, inside, acc, hist, lists[wave]);
-        if (inside) {
+            const int stop = min(end, round_end);
+            if (inside && t >= pos && t < stop) {
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                lists[wave].place[j][lane] = __float_as_uint(acc[j]);
-                acc[j] = 0.0f;
+                for (int j = 0; j < J; ++j) acc[j] = __builtin_fmaf(v[j], inv, acc[j]);
+                if (lane < a.topk && logit != -INFINITY) atomicAdd(hist + id, 1);
             }
-            __syncthreads();
-            const size_t at = (size_t(blockIdx.x) + s) * a.n_expert;
-            for (int e = threadIdx.x; e < a.n_expert; e += kThreads) {
-                const int j = e % J, l = e / J;
-                float p = __uint_as_float(lists[0].place[j][l]);
+            if (inside && stop == end) {
 #pragma unroll
-                for (int w = 1; w < kWaves; ++w) p += __uint_as_float(lists[w].place[j][l]);
-                out_p[at + e] = p;
-                out_c[at + e] = hist[e];
-                hist[e] = 0;
+                for (int j = 0; j < J; ++j) {
+                    lists[wave].place[j][lane] = __float_as_uint(acc[j]);
+                    acc[j] = 0.0f;
+                }
+                __syncthreads();
+                const size_t at = (size_t(blockIdx.x) + s) * a.n_expert;
+                for (int e = threadIdx.x; e < a.n_expert; e += kThreads) {
+                    const int j = e % J, l = e / J;
+                    float p = __uint_as_float(lists[0].place[j][l]);
+#pragma unroll
+                    for (int w = 1; w < kWaves; ++w) p += __uint_as_float(lists[w].place[j][l]);
+                    out_p[at + e] = p;
+                    out_c[at + e] = hist[e];
+                    hist[e] = 0;
+                }
+                __syncthreads();
             }
-            __syncthreads();
+            pos = stop;
         }
-        pos = end;
     }
 }
 
@@ -449,17 +463,19 @@ __global__ __launch_bounds__(64 * kJoinWaves) void balance_join_kernel(RouteArgs
                                             __HIP_MEMORY_SCOPE_AGENT) == int(gridDim.x) - 1;
     __syncthreads();
     if (!last_group) return;
-    double *sums = red_p;
     double sum = 0.0;
     for (int64_t i = threadIdx.x; i < jobs; i += 64 * kJoinWaves)
         sum += double(__hip_atomic_load(loss + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-    sums[threadIdx.x] = sum;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d);
+    if (lane == 0) red_p[wave] = sum;
     __syncthreads();
-    for (int half = 32 * kJoinWaves; half > 0; half >>= 1) {
-        if (int(threadIdx.x) < half) sums[threadIdx.x] += sums[threadIdx.x + half];
-        __syncthreads();
+    if (threadIdx.x == 0) {
+        sum = red_p[0];
+#pragma unroll
+        for (int i = 1; i < kJoinWaves; ++i) sum += red_p[i];
+        a.loss[0] = float(double(a.coef) / a.n_seq * sum);
     }
-    if (threadIdx.x == 0) a.loss[0] = float(double(a.coef) / a.n_seq * sums[0]);
 }
 
 // The gradient of one token's row.  The chosen experts' parts are scattered
