@@ -115,7 +115,10 @@ struct AdapterSplit {
 // rows 55.5 and 58.
 constexpr int kAdapterLongRows = 8192;
 constexpr int kAdapterStep = 128;        // 4 waves x 32 values: what a slice is a multiple of
-constexpr int kAdapterGroups = 512;      // workgroups a launch should have, two per CU
+// Workgroups a launch should have, one per CU: more slices are more planes to
+// add in the update (1,024 / 2,048 fp32 rows at rank 64: 18.1 / 28.4 us with
+// two per CU, 15.6 / 25.2 with one).
+constexpr int kAdapterGroups = 256;
 inline AdapterSplit adapter_split(int tokens, int n_in) {
     AdapterSplit s{};
     s.row_groups = tokens > kAdapterLongRows ? 2 : 1;
