@@ -134,6 +134,25 @@ def test_many_rows(T, rank, dtype, wdtype):
     assert torch.equal(run(d, T), out[perm])
 
 
+@pytest.mark.parametrize("T,n,rank", [(257, 48, 72), (512, 5, 16), (700, 300, 40), (1000, 1000, 8), (1023, 1023, 24),
+                                      (1024, 1022, 16), (1024, 1024, 16), (1025, 48, 16)])
+@pytest.mark.parametrize("kind", ["mixed", "own", "two"])
+def test_batches_in_any_order(T, n, rank, kind):
+    """Hundreds of new tokens, their adapters in no order: taken by adapter up to 1,024 rows and 1,023
+    adapters, in tiles of neighbours beyond, with the same results."""
+    rng = np.random.default_rng(T + n)
+    ids = {"mixed": rng.integers(-1, n, T), "own": rng.permutation(T) % n,
+           "two": np.where(rng.random(T) < 0.5, 0, n - 1)}[kind]
+    print("adapters in any order", T, n, rank, kind, flush=True)
+    d, want = make(T, n, rank, 264, 1096, "f32", "bf16", ids, seed=T)
+    out = run(d, T)
+    check(out, want, "f32", 264, rank)
+    order = torch.from_numpy(np.argsort(ids, kind="stable")).cuda()
+    for k in ("ids", "x", "base"):
+        d[k] = d[k][order].contiguous()
+    assert torch.equal(run(d, T), out[order])
+
+
 def test_strided_and_interleaved_rows():
     """x, base and out as column slices of one buffer; columns between them stay."""
     T, n, rank, n_in, n_out = 40, 3, 16, 72, 88
