@@ -106,18 +106,33 @@ def _rows(device: int, t, what: str, shape, written: bool = False):
     if t.shape != shape:
         raise MoeError(-1, f"{what}: shape {tuple(t.shape)}; {tuple(shape)} wanted")
     ld, step = t.stride()
-    if (step != 1 and shape[1] > 1) or (written and ld < shape[1] and shape[0] > 1):
+    if (step != 1 and shape[1] > 1 and shape[0] > 0) or (written and ld < shape[1] and shape[0] > 1):
         raise MoeError(-1, f"{what}: strides {t.stride()}; dense rows wanted")
     if t.get_device() != device:
         raise MoeError(-1, f"{what}: on {t.device}, the current device is cuda:{device}")
-    # the stride of a single row says nothing: torch may give it any value
+    # the strides of no row, and a single row's, say nothing: torch may give them any value
     return t.data_ptr(), ld if shape[0] > 1 else shape[1]
+
+
+def _count(n: int, what: str) -> int:
+    """n as the C call takes it: ctypes would cut a larger one to its low 32 bits."""
+    if n > 0x7fffffff:
+        raise MoeError(-1, f"{what}: {n} rows")
+    return n
 
 
 def _matrix(t, what: str):
     if t is None or t.dim() != 2:
         raise MoeError(-1, f"{what}: {None if t is None else tuple(t.shape)} is not a matrix")
-    return t.shape
+    shape = t.shape
+    _count(shape[0], what)
+    return shape
+
+
+def _sequences(seq_off) -> int:
+    if seq_off is None:
+        raise MoeError(-1, "seq_off: None")
+    return _count(seq_off.numel() - 1, "seq_off")
 
 
 def _route(device: int, logits, topk: int, renorm: bool, scale: float):
@@ -152,7 +167,7 @@ def moe_route_balance(logits, seq_off, coef: float, ids, w, counts, probs, loss,
     dev, raw = _current(stream, logits, "logits")
     K = _matrix(ids, "ids")[1]
     head = _route(dev, logits, K, renorm, scale)
-    T, E, S = head[3], head[4], seq_off.numel() - 1
+    T, E, S = head[3], head[4], _sequences(seq_off)
     f32, i32 = torch.float32, torch.int32
     st = lib().moe_route_balance(
         *head, _dense(dev, seq_off, "seq_off", i32, (S + 1,)), S, coef, _dense(dev, ids, "ids", i32, (T, K)),
@@ -183,8 +198,10 @@ def moe_route_backward(logits, ids, dw, dlogits, renorm: bool = True, scale: flo
     K = _matrix(ids, "ids")[1]
     head = _route(dev, logits, K, renorm, scale)
     T, E = head[3], head[4]
-    S = 0 if seq_off is None else seq_off.numel() - 1
+    S = 0 if seq_off is None else _sequences(seq_off)
     f32, i32 = torch.float32, torch.int32
+    if dlogits is None:
+        raise MoeError(-1, "dlogits: None")
     if dlogits.dtype != logits.dtype:
         raise MoeError(-3, f"dlogits: {dlogits.dtype} instead of {logits.dtype}")
     d_ptr, ldd = _rows(dev, dlogits, "dlogits", (T, E), True)
@@ -218,8 +235,9 @@ class AdapterSet:
 
     def __init__(self, a, b, scale, rank=None):
         torch = _load_torch()
-        if a.dim() != 3 or b.dim() != 3:
-            raise MoeError(-1, f"AdapterSet: a {tuple(a.shape)}, b {tuple(b.shape)}")
+        if any(t is None or t.dim() != 3 for t in (a, b)):
+            raise MoeError(-1, "AdapterSet: a and b " + " ".join("None" if t is None else str(tuple(t.shape))
+                                                                  for t in (a, b)))
         n, r, n_in = a.shape
         n_out = b.shape[1]
         code = _dtype(a, "a")
@@ -246,7 +264,9 @@ def moe_adapters(adapters: AdapterSet, ids, x, base, out, workspace, stream=None
     dev, raw = _current(stream, x, "x")
     if adapters.device != dev:
         raise MoeError(-1, f"adapters: on cuda:{adapters.device}, the current device is cuda:{dev}")
-    T = ids.numel()
+    if ids is None or base is None or out is None:
+        raise MoeError(-1, "moe_adapters: ids, base and out are needed")
+    T = _count(ids.numel(), "ids")
     kind = x.dtype
     if base.dtype != kind or out.dtype != kind:
         raise MoeError(-3, f"moe_adapters: x {x.dtype}, base {base.dtype}, out {out.dtype}")

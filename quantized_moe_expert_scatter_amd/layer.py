@@ -142,6 +142,8 @@ class DeviceLayer:
     def backward(self, dout, stream=None, dloss=None):
         """The gradient of the output (dout, float32 [T, hidden] on the device)
         and of the balance loss (dloss, float32 [1], None for 1) -> dlogits."""
+        if self.logits is None:
+            raise ValueError("backward: the layer was not built from logits")
         _steps.moe_combine_backward(self.dm[:self.rows], self.route_w, dout, self.dw, stream=stream)
         _steps.moe_route_backward(self.logits, self.ids_dev, self.dw, self.dlogits, renorm=self.renorm,
                                   seq_off=self.seq_off, coef=self.balance_coef,

@@ -148,6 +148,25 @@ def test_captured_and_replayed():
     assert G.check_guards() == []
 
 
+def test_empty_layer_and_one_without_logits():
+    """No tokens: every step runs, the statistics are zeros.  Without logits there is nothing to go back to."""
+    hidden, n_ff, E, K = 128, 64, 8, 2
+    L = wl.make_layer(wl.small_config("empty", 4, hidden, n_ff, E, K, seed=1))
+    _, _, _, adapters = make_adapters(2, 8, hidden, seed=8)
+    D = DeviceLayer(L.x[:0], None, L.w_gu, L.w_down, chunk_rows=64, guard=GUARD, logits=np.zeros((0, E), np.float32),
+                    topk=K, seq_off=np.zeros(3, np.int32), balance_coef=0.1, adapters=adapters,
+                    adapter_ids=np.zeros(0, np.int32))
+    D.forward()
+    assert D.backward(torch.zeros(0, hidden, device="cuda")).shape == (0, E)
+    torch.cuda.synchronize()
+    assert not D.counts.any() and not D.probs.any() and float(D.loss) == 0.0
+    D.close()
+    D = DeviceLayer(L.x, L.ids, L.w_gu, L.w_down, chunk_rows=64)
+    with pytest.raises(ValueError):
+        D.backward(torch.zeros(4, hidden, device="cuda"))
+    D.close()
+
+
 @pytest.mark.parametrize("T,rank,dtype", [(300, 24, torch.float32), (300, 72, torch.bfloat16), (8200, 48, torch.float32)])
 def test_long_batches_captured(T, rank, dtype):
     """The adapters' two-launch forms and the combine's gradient with the rows', replayed over changed inputs."""

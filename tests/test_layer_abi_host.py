@@ -195,6 +195,12 @@ def test_binding_refuses_what_the_c_call_cannot_see():
     assert status(_steps.AdapterSet, a[0], b, s) == EINVAL
     assert status(_steps.AdapterSet, a.float(), b, s) == EFORMAT
     assert status(_steps.AdapterSet, a, b, s) == EINVAL
+    assert status(_steps.AdapterSet, None, b, s) == EINVAL
+    assert status(_steps.AdapterSet, a, None, s) == EINVAL
+    # row counts past an int, which ctypes would cut to 1
+    assert status(_steps._matrix, torch.empty((1 << 32) + 1, 1, device="meta"), "logits") == EINVAL
+    assert status(_steps._sequences, torch.empty((1 << 32) + 2, device="meta")) == EINVAL
+    assert status(_steps._sequences, None) == EINVAL
 
 
 # ------------------------------------------------ the plain forms themselves
