@@ -83,6 +83,7 @@ __global__ __launch_bounds__(kCombineThreads) void combine_kernel(const float *d
 // NB rows of one token per wave (all of them clamped to the last, so that their
 // loads are in flight together): the output gradient's chunk stays in registers
 // while the rows' chunks pass; the NB sums are joined over the lanes at the end.
+// A lane reads its part of a row before it writes it, so ddm may be dm itself.
 // SPLIT: few tokens, the four waves of a workgroup share the columns of the
 // same rows and are added through LDS.
 template <int NB, bool DW, bool DDM, bool SPLIT, bool STREAM>

@@ -264,6 +264,21 @@ def test_combine_backward(hidden, T, K):
             assert np.array_equal(ddm[:T * K].cpu().numpy(), want_ddm)
 
 
+@pytest.mark.parametrize("T,K,hidden", [(1, 1, 4), (7, 10, 252), (64, 33, 2560), (2500, 10, 1280)])
+def test_combine_backward_in_place(T, K, hidden):
+    """ddm in dm's own buffer: few tokens, many, and rows past the caches give what separate buffers give."""
+    print("combine backward in place", T, K, hidden, flush=True)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    dm = torch.randn(T * K, hidden, device="cuda", generator=g)
+    w = torch.randn(T, K, device="cuda", generator=g)
+    do = torch.randn(T, hidden, device="cuda", generator=g)
+    want_dw, want = torch.empty_like(w), torch.empty_like(dm)
+    moe.moe_combine_backward(dm, w, do, want_dw, want)
+    dw = torch.empty_like(w)
+    moe.moe_combine_backward(dm, w, do, dw, dm)
+    assert torch.equal(dw, want_dw) and torch.equal(dm, want)
+
+
 def test_same_bits_every_time():
     """Fixed orders of summation: a second run, and one on another stream, give the same bits."""
     T, E, K, S = 3000, 512, 10, 3
