@@ -19,10 +19,10 @@ namespace {
 constexpr int kThreads = 256;
 // The single launch computes a row's h in each of its output slices, so it is
 // taken while tokens * rank * slices is small.  Measured at 2560 -> 2560 (3
-// slices), rows of one adapter / every row its own: rank 16, 256 rows 9.4 /
-// 12.4 us in one launch, 257 rows 8.5 / 35 in two; rank 32, 128 rows 10.1 /
-// 14.2 in one, 200 rows 9.9 / 20.4 in two; rank 64, 64 rows 11.3 / 16.9 in one,
-// 128 rows 20.5 / 29.0 in one and 10.9 / 21.4 in two.
+// slices), rows of one adapter / of 48 in any order: rank 16, 256 rows 9.3 /
+// 12.4 us in one launch, 257 rows 9.2 / 20.1 in two; rank 32, 128 rows 9.7 /
+// 14.0 in one, 200 rows 9.7 / 20.8 in two; rank 64, 64 rows 10.8 / 16.6 in one,
+// 128 rows 20.5 / 29.0 in one and 10.8 / 23.8 in two.
 constexpr int kFewRows = 256;
 constexpr int kFewValues = 12288;
 
@@ -848,7 +848,7 @@ hipError_t launch_adapters(const AdapterArgs &g, hipStream_t stream) {
         using Four = std::integral_constant<int, 4>;
         // workgroups that share a tile's passes (one for each of its adapters):
         // rows by adapter need few, and each workgroup has to find its rows (1,024
-        // rows in any order 44 us with 4, 49 with 16)
+        // rows in any order 44 us with 4, 50 with 16)
         auto passes = [&](int64_t groups) {
             const int64_t most = g.tokens <= kSortRows ? 4 : 16, n = 2048 / groups;
             return unsigned(n < 1 ? 1 : n > most ? most : n);
