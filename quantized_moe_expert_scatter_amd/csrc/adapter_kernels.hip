@@ -486,12 +486,15 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterArgs g, A
 // b turned through LDS as in the other kernel level (11.1).
 constexpr int kUpRank = 64;          // rank values of h in LDS at a time
 constexpr int kUpStride = kUpRank + 4;
+// Parts of h: all of its fp32, for 16-bit rows too, where the third shows only if
+// base takes most of the update away (2,047 bf16 rows at rank 64 24.0 us with two
+// parts, 24.9 with three; 2,047 fp16 rows at rank 24 16.9 and 17.1).
+constexpr int kHP = 3;
 
 template <int XT, int WT, int KB>
 __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterArgs g, AdapterSplit s, int tiles, int slices,
                                                               int per) {
     using T = typename Elem<XT>::T;
-    constexpr int kHP = XT == kF32 ? 3 : 2;      // 16 bits of h are enough for 16-bit rows
     constexpr int kRun = XT == kF32 ? 4 : 8;     // 16 bytes of a row
     constexpr int kLanes = 64 / kRun;            // lanes of a row's 64 outputs
     constexpr int kRows = 64 / kLanes;           // rows of one access
@@ -664,7 +667,6 @@ constexpr int kWideGroups = 4096;
 template <int XT, int WT, int KB>
 __global__ __launch_bounds__(kThreads) void adapter_up_wide_kernel(AdapterArgs g, AdapterSplit s, int slices, int per) {
     using T = typename Elem<XT>::T;
-    constexpr int kHP = XT == kF32 ? 3 : 2;
     constexpr int kRun = XT == kF32 ? 4 : 8;     // 16 bytes of a row
     constexpr int kLanes = 64 / kRun;            // lanes of a row's 64 outputs
     constexpr int kRows = 64 / kLanes;           // rows of one access

@@ -1,0 +1,56 @@
+"""Adapters: what the two-launch forms must keep, which small batches do not
+reach.  Batches of 300 rows take the 16-row update, 8,200 rows the 64-row one
+(ranks up to 64), rank 72 the update for any rank.
+
+Bounds: u = 2^-24 is half a step of fp32."""
+import numpy as np
+import pytest
+import torch
+
+import quantized_moe_expert_scatter_amd as moe
+from tests import layer_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+TYPES = [("f32", "bf16"), ("f32", "f16"), ("bf16", "bf16"), ("f16", "f16")]
+FORMS = [(300, 8), (300, 24), (300, 48), (300, 72), (8200, 24), (8200, 64), (8200, 72)]
+
+
+def run(a, b, scale, ids, x, base, ranks=None):
+    s = moe.AdapterSet(a, b, scale, rank=ranks)
+    T = ids.numel()
+    ws = torch.full((moe.moe_adapters_bytes(s, T),), 0xFF, dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(base)
+    moe.moe_adapters(s, ids, x, base, out, ws)
+    torch.cuda.synchronize()
+    return out
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("T,rank", FORMS)
+def test_low_rank_values_of_16_bit_rows_are_fp32(T, rank, dtype):
+    """base takes the update away but for its own rounding, so that the result shows the update's
+    low bits.  Every factor is positive: the update's magnitudes are the update itself, and a
+    sum of n_in, then rank terms, the scale and the base's addition stay within
+    (n_in + rank + 8) u of it; the result is rounded once."""
+    print("16-bit rows", T, rank, dtype, flush=True)
+    n_in, n_out, dt = 16, 72, DT[dtype]
+    rng = np.random.default_rng(T + rank)
+    pos = lambda *shape: torch.from_numpy(rng.random(shape) + 0.5).to(dt)
+    a, b, x = pos(2, rank, n_in), pos(2, n_out, rank) / 64, pos(T, n_in)
+    scale = torch.tensor([0.75, 1.25])
+    ids = torch.from_numpy(rng.integers(0, 2, T).astype(np.int32))
+    i = ids.long()
+    update = np.empty((T, n_out))
+    for k in range(2):
+        on = np.nonzero(i.numpy() == k)[0]
+        h = x.double().numpy()[on] @ a[k].double().numpy().T
+        update[on] = float(scale[k]) * (h @ b[k].double().numpy().T)
+    base = torch.from_numpy(-update).to(dt)
+    want = base.double().numpy() + update
+    out = run(*(t.cuda() for t in (a, b, scale, ids, x, base))).double().cpu().numpy()
+    tiny = 2.0 ** -25 if dtype == "f16" else 0.0
+    tol = update * (n_in + rank + 8) * ref.U + np.abs(want) * ref.HALF[dtype] * 1.01 + tiny
+    err = np.abs(out - want)
+    assert np.all(err <= tol), (np.max(err / tol), np.mean(err > tol))
