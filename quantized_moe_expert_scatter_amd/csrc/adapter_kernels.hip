@@ -191,15 +191,17 @@ template <int WT> struct Weight {
     }
 };
 
-// c += w * v over bf16 parts, the smallest first; products below 2^-24 of the
-// largest (part indexes adding up to 3 or more) are left out.
+// c += w * v over all pairs of bf16 parts, the smallest first.  (That of the
+// second part of w and the third of v reaches 2^-22.1 of the whole, always with
+// its sign; 16,384 fp32 rows at rank 64 with fp16 matrices take 132 us with it and
+// 129 without.)
 template <int WP, int VP>
 __device__ __forceinline__ f32x4 mfma_parts(const u32x4 (&w)[WP], const u32x4 (&v)[VP], f32x4 c) {
 #pragma unroll
     for (int s = WP + VP - 2; s >= 0; --s)
 #pragma unroll
         for (int i = 0; i < WP; ++i)
-            if (s - i >= 0 && s - i < VP && s < 3) c = mfma_bf16(w[i], v[s - i], c);
+            if (s - i >= 0 && s - i < VP) c = mfma_bf16(w[i], v[s - i], c);
     return c;
 }
 

@@ -54,3 +54,25 @@ def test_low_rank_values_of_16_bit_rows_are_fp32(T, rank, dtype):
     tol = update * (n_in + rank + 8) * ref.U + np.abs(want) * ref.HALF[dtype] * 1.01 + tiny
     err = np.abs(out - want)
     assert np.all(err <= tol), (np.max(err / tol), np.mean(err > tol))
+
+
+@pytest.mark.parametrize("T,rank", FORMS)
+@pytest.mark.parametrize("where", ["a", "b"])
+def test_fp16_matrices_beside_fp32_values_lose_nothing(T, rank, where):
+    """One product per result: w = 1 + 7/1024 is two bf16 parts, v = 1 + 2^-8 + .. three, the last of
+    255 * 2^-23, so that the product of their low parts is 3.45 u of the whole and always of the same sign.  Kept,
+    the result is off by the last addition (at most a whole step, 2 u, if it truncates) and by the
+    others, below 2^-8 of that; the two uses of w have nothing else to round."""
+    print("fp16 matrices", T, rank, where, flush=True)
+    n_in, n_out = 8, 72
+    w = 1.0 + 7.0 / 1024
+    a, b = torch.zeros(1, rank, n_in, dtype=torch.float16), torch.zeros(1, n_out, rank, dtype=torch.float16)
+    a[0, 0, 0] = w if where == "a" else 1.0
+    b[0, :, 0] = w if where == "b" else 1.0
+    x = torch.zeros(T, n_in)
+    x[:, 0] = 1.0 + 2.0 ** -8 + torch.arange(T) % 8 * 2.0 ** -14 + 255 * 2.0 ** -23      # below 1.005
+    want = x[:, :1].double() * w
+    out = run(a.cuda(), b.cuda(), torch.ones(1, device="cuda"), torch.zeros(T, dtype=torch.int32, device="cuda"),
+              x.cuda(), torch.zeros(T, n_out, device="cuda")).double().cpu()
+    off = ((out - want) / want).abs().max().item() / ref.U
+    assert off <= 2.0 * (1 + 2.0 ** -7), off
