@@ -336,32 +336,34 @@ route_balance_kernel(RouteArgs a, BalanceLayout L) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     float *out_p = reinterpret_cast<float *>(a.ws + L.probs);
     int32_t *out_c = reinterpret_cast<int32_t *>(a.ws + L.counts);
+    // rows are counted from the range's first: their numbers may reach 2^31 - 1, and a position a
+    // round further on would not be one
     const int t0 = int(blockIdx.x) * L.range_tokens;
-    const int t1 = a.tokens - t0 < L.range_tokens ? a.tokens : t0 + L.range_tokens;
+    const int rows = min(a.tokens - t0, L.range_tokens);
     for (int e = threadIdx.x; e < 64 * J; e += kThreads) hist[e] = 0;
     __syncthreads();
     float acc[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) acc[j] = 0.0f;
-    int s = 0, end = t0;                       // the sequence at hand ends (or leaves the range) there
+    int s = 0, end = 0;                        // the sequence at hand ends (or leaves the range) there
     bool inside = false;
-    for (int round = t0; round < t1; round += kWaves) {
-        const int t = round + wave, round_end = t1 - round < kWaves ? t1 : round + kWaves;
+    for (int round = 0; round < rows; round += kWaves) {
+        const int t = round + wave, round_end = min(rows, round + kWaves);
         float v[J], inv = 0.0f, logit = -INFINITY;
         int id = 0;
-        if (t < round_end) route_token<J, DT, VEC, true>(a, t, lane, v, inv, id, logit, lists[wave]);
+        if (t < round_end) route_token<J, DT, VEC, true>(a, t0 + t, lane, v, inv, id, logit, lists[wave]);
         for (int pos = round; pos < round_end;) {
             if (pos >= end) {
-                s = sequence_of(a.seq_off, a.n_seq, pos, lane);
+                s = sequence_of(a.seq_off, a.n_seq, t0 + pos, lane);
                 inside = s < a.n_seq;
-                end = t1;
+                end = rows;
                 if (inside) {
                     const int b = a.seq_off[s], e = a.seq_off[s + 1];
-                    if (pos < b) {              // in front of the first sequence
+                    if (t0 + pos < b) {         // in front of the first sequence
                         inside = false;
-                        end = min(b, t1);
-                    } else if (e > pos) {
-                        end = min(e, t1);
+                        end = min(b - t0, rows);
+                    } else if (e > t0 + pos) {
+                        end = min(e - t0, rows);
                     }
                 }
             }
