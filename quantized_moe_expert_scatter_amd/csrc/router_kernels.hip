@@ -259,18 +259,19 @@ __device__ __forceinline__ float exp_neg(float x) {
 }
 
 // First sequence with seq_off[s+1] > t (n_seq if none), by 64 probes a step.
+// Unsigned: 64 steps may pass 2^31, by less than 64.
 __device__ __forceinline__ int sequence_of(const int32_t *seq_off, int n_seq, int t, int lane) {
-    int lo = 0, n = n_seq;              // the answer is in [lo, lo + n]
+    uint32_t lo = 0, n = n_seq;         // the answer is in [lo, lo + n]
     while (n > 0) {
-        const int step = (n + 63) / 64;
-        const int i = lo + (lane + 1) * step - 1;
-        const bool past = lane * step < n && seq_off[1 + min(i, lo + n - 1)] <= t;
-        const int skip = __popcll(__ballot(past)) * step;
-        if (skip >= n) return lo + n;
+        const uint32_t step = (n + 63) / 64;
+        const uint32_t i = lo + uint32_t(lane + 1) * step - 1;
+        const bool past = uint32_t(lane) * step < n && seq_off[1 + min(i, lo + n - 1)] <= t;
+        const uint32_t skip = uint32_t(__popcll(__ballot(past))) * step;
+        if (skip >= n) return int(lo + n);
         lo += skip;
         n = min(step - 1, n - skip);
     }
-    return lo;
+    return int(lo);
 }
 
 // Routes token t.  With STATS it returns the row's softmax, v * inv, and lane
