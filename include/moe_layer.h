@@ -110,9 +110,9 @@ int moe_route_backward(const void *logits, int64_t ld, int dtype, int tokens, in
  * [tokens x topk]; dout: device fp32 [tokens x hidden]; hidden % 4 == 0
  * (MOE_EFORMAT).  dw or ddm may be NULL (not both): without dw, dm may be
  * NULL; without ddm, w may be.  ddm may be dm itself (dw is that of the rows as
-they were).  MOE_EINVAL if tokens * topk exceeds 2^30 or
- * tokens * ceil(topk / 8) reaches 2^26 (the launch's thread count).  No plan
- * is needed, so the backward pass of a layer may run after its plan is gone. */
+ * they were).  MOE_EINVAL if tokens * topk exceeds 2^30 or tokens *
+ * ceil(topk / 8) exceeds 2^26 - 4 (the launch's thread count).  No plan is
+ * needed, so the backward pass of a layer may run after its plan is gone. */
 int moe_combine_backward(const float *dm, const float *w, const float *dout, int tokens, int topk,
                          int hidden, float *dw, float *ddm, void *stream);
 

@@ -123,8 +123,9 @@ int moe_combine_backward(const float *dm, const float *w, const float *dout, int
                          int hidden, float *dw, float *ddm, void *stream) {
     if (tokens < 0 || topk <= 0 || hidden <= 0) return MOE_EINVAL;
     if ((long long)tokens * topk > (1LL << 30)) return MOE_EINVAL;     // as a plan's rows
-    // one wave per token and eight of its rows: a launch holds 2^32 - 1 threads
-    if ((long long)tokens * ((topk + 7) / 8) >= (1LL << 26)) return MOE_EINVAL;
+    // one wave per token and eight of its rows, four to a workgroup: a launch holds 2^32 - 1 threads,
+    // so 2^24 - 1 workgroups
+    if ((long long)tokens * ((topk + 7) / 8) > (1LL << 26) - 4) return MOE_EINVAL;
     if (hidden % 4) return MOE_EFORMAT;
     if (tokens == 0) return MOE_OK;
     if (!dout || (!dw && !ddm) || (dw && !dm) || (ddm && !w)) return MOE_EINVAL;
