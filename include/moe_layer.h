@@ -59,7 +59,9 @@ enum { MOE_ROUTE_RENORM = 1 };
 int moe_route(const void *logits, int64_t ld, int dtype, int tokens, int n_expert, int topk,
               int flags, float scale, int32_t *ids, float *w, void *stream);
 
-/* Workspace of moe_route_balance (0 on invalid sizes). */
+/* Workspace of moe_route_balance (0 on invalid sizes).  It does not shrink as
+ * tokens or n_seq grow: that of the largest batch serves every smaller one of
+ * the same n_expert. */
 size_t moe_balance_bytes(int tokens, int n_expert, int n_seq);
 
 /* moe_route with the balance statistics of the batch's n_seq sequences.
@@ -74,8 +76,8 @@ size_t moe_balance_bytes(int tokens, int n_expert, int n_seq);
  *                 sum over e of (counts * n_expert / (topk * n_s)) * probs
  * (1 * coef when every expert is chosen equally often).  An empty sequence
  * has zero counts and probs and adds nothing.  n_seq >= 1.
- *   workspace     device, moe_balance_bytes(tokens, n_expert, n_seq) bytes,
- *                 16-byte aligned, free again when the call's work has run */
+ *   workspace     device, moe_balance_bytes(tokens, n_expert, n_seq) bytes
+ *                 or more, 16-byte aligned, free again when the call's work has run */
 int moe_route_balance(const void *logits, int64_t ld, int dtype, int tokens, int n_expert, int topk,
                       int flags, float scale, const int32_t *seq_off, int n_seq, float coef,
                       int32_t *ids, float *w, int32_t *counts, float *probs, float *loss,
@@ -138,7 +140,8 @@ typedef struct {
     const int32_t *ranks;
 } moe_adapter_set;
 
-/* Workspace of moe_adapters over `tokens` rows (0 on invalid sizes). */
+/* Workspace of moe_adapters over up to `tokens` rows (0 on invalid sizes): that
+ * of the largest batch serves every smaller one of the same set. */
 size_t moe_adapters_bytes(const moe_adapter_set *set, int tokens);
 
 /* Low-rank adapters of many requests beside a projection all of them share
@@ -155,7 +158,7 @@ size_t moe_adapters_bytes(const moe_adapter_set *set, int tokens);
  *   out    base itself (same pointer and stride: rows without an adapter are
  *          then left as they are) or memory that shares no element with base;
  *          it shares none with x
- *   workspace  device, moe_adapters_bytes(set, tokens) bytes, 16-byte
+ *   workspace  device, moe_adapters_bytes(set, tokens) bytes or more, 16-byte
  *          aligned, free again when the call's work has run
  * a * x is held in fp32, the result rounded once.  What a row holds reaches no
  * other row; an infinity in fp32 x may give NaN where the formula has an

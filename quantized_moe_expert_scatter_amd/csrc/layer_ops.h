@@ -50,10 +50,12 @@ constexpr int balance_waves(int lane_experts) {
 // of range_tokens, one workgroup each, and a range's part of a sequence is a
 // piece.  Sequences are in token order, so (range, sequence) -> range +
 // sequence numbers the pieces without collisions, and no kernel needs to know
-// on the host where sequences begin.
+// on the host where sequences begin.  There is room for as many ranges as any
+// smaller batch has: the longer ranges of a batch that is just too long for 512
+// of the shortest are fewer.
 struct BalanceLayout {
     int range_tokens, n_ranges;
-    size_t probs;      // fp32 [n_ranges + n_seq][E]: sums of p over a piece
+    size_t probs;      // fp32 [ranges + n_seq][E]: sums of p over a piece
     size_t counts;     // int32, the same shape
     size_t loss;       // fp32 [n_seq][column blocks]: parts of the loss
     size_t done;       // int32: joining workgroups that have written theirs
@@ -69,7 +71,9 @@ inline BalanceLayout balance_layout(int tokens, int n_expert, int n_seq) {
     const long long per = ((long long)tokens + kBalanceMaxRanges - 1) / kBalanceMaxRanges;
     L.range_tokens = per > waves ? int((per + waves - 1) / waves * waves) : waves;
     L.n_ranges = int(((long long)tokens + L.range_tokens - 1) / L.range_tokens);
-    const size_t cells = (size_t(L.n_ranges) + size_t(n_seq)) * size_t(n_expert);
+    const long long most = ((long long)tokens + waves - 1) / waves;
+    const size_t ranges = size_t(most < kBalanceMaxRanges ? most : kBalanceMaxRanges);
+    const size_t cells = (ranges + size_t(n_seq)) * size_t(n_expert);
     auto up = [](size_t x) { return (x + 15) & ~size_t(15); };
     size_t o = 0;
     L.probs = o;  o += up(cells * 4);
@@ -132,9 +136,21 @@ inline AdapterSplit adapter_split(int tokens, int n_in) {
     s.splits = (steps + per - 1) / per;
     return s;
 }
-inline size_t adapter_workspace(int tokens, int rank, int n_in) {
+// What a call over so many rows uses, and what any call over up to so many does:
+// fewer rows are cut into more slices (2,049 of 2560 into 2, 4,096 into 1).
+inline size_t adapter_planes(int tokens, int rank, int n_in) {
     const size_t planes = size_t(adapter_split(tokens, n_in).splits);
     return (planes * size_t(tokens) * size_t(rank) * 4 + 15) & ~size_t(15);
+}
+static_assert(kAdapterLongRows >= 16 * kAdapterGroups, "one slice where tiles have more than 16 rows");
+inline size_t adapter_workspace(int tokens, int rank, int n_in) {
+    size_t most = adapter_planes(tokens, rank, n_in);
+    // the fullest of each number of tiles that has more than one slice
+    for (int t = 16; t < tokens && t < 16 * kAdapterGroups; t += 16) {
+        const size_t b = adapter_planes(t, rank, n_in);
+        if (b > most) most = b;
+    }
+    return most;
 }
 hipError_t launch_adapters(const AdapterArgs &a, hipStream_t stream);
 

@@ -160,7 +160,7 @@ int moe_adapters(const moe_adapter_set *set, const int32_t *ids, int tokens, int
     if (out == x || (out == base && ldo != ldb)) return MOE_EINVAL;
     if (!aligned16(ids) || !aligned16(x) || !aligned16(base) || !aligned16(out) || !aligned16(workspace))
         return MOE_EALIGN;
-    if (workspace_bytes < adapter_workspace(tokens, set->rank, set->n_in)) return MOE_ESIZE;
+    if (workspace_bytes < adapter_planes(tokens, set->rank, set->n_in)) return MOE_ESIZE;
     AdapterArgs a{};
     a.wtype = set->dtype; a.dtype = dtype;
     a.n_adapter = set->n_adapter; a.rank = set->rank; a.n_in = set->n_in; a.n_out = set->n_out;

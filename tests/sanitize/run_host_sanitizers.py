@@ -25,7 +25,7 @@ ROOT = os.path.dirname(os.path.dirname(os.path.dirname(os.path.abspath(__file__)
 SAN = ["-fsanitize=address,undefined", "-fno-sanitize-recover=all", "-fno-omit-frame-pointer", "-g"]
 TESTS = ["tests/test_oracle_q8_1.py", "tests/test_oracle_weights.py", "tests/test_oracle_products.py",
          "tests/test_oracle_swiglu_plan.py", "tests/test_oracle_combine.py", "tests/test_abi_host.py",
-         "tests/test_layer_abi_host.py"]
+         "tests/test_layer_abi_host.py", "tests/test_layer_abi_limits_host.py"]
 
 
 def main() -> int:

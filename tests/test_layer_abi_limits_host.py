@@ -1,10 +1,39 @@
 """The C ABI of include/moe_layer.h on the host (no GPU), at its limits."""
+import ctypes
+
 import pytest
 
-from tests.test_layer_abi_host import EINVAL, combine
+from quantized_moe_expert_scatter_amd import _steps
+from tests.test_layer_abi_host import EINVAL, ESIZE, adapters, combine, make_set
 
 
 @pytest.mark.parametrize("tokens,topk", [((1 << 26) - 3, 1), ((1 << 26) - 2, 8), ((1 << 26) - 1, 5), ((1 << 25) - 1, 9)])
 def test_combine_backward_refuses_a_launch_of_2_to_32_threads(tokens, topk):
     """A wave per token and eight rows, four to a workgroup of 256: 2^24 workgroups are one too many."""
     assert combine(tokens=tokens, topk=topk) == EINVAL
+
+
+@pytest.mark.parametrize("E,S", [(8, 1), (100, 5), (512, 1), (1000, 2), (2048, 3)])
+def test_balance_workspace_of_a_batch_serves_every_smaller_one(E, S):
+    sizes = [_steps.moe_balance_bytes(T, E, S) for T in [*range(0, 20000, 7), *range(20000, 2 ** 22, 9973), 2 ** 31 - 1]]
+    assert sizes == sorted(sizes) and sizes[0] > 0
+    some = [_steps.moe_balance_bytes(12345, E, s) for s in range(1, 200)]
+    assert some == sorted(some)
+
+
+@pytest.mark.parametrize("rank,n_in", [(8, 8), (64, 2560), (24, 1160), (256, 1 << 24)])
+def test_adapter_workspace_of_a_batch_serves_every_smaller_one(rank, n_in):
+    s = make_set(rank=rank, n_in=n_in)
+    size = lambda T: _steps.lib().moe_adapters_bytes(ctypes.byref(s), T)
+    sizes = [size(T) for T in [*range(0, 9000), *range(9000, 1 << 24, 99991), 1 << 24]]
+    assert sizes == sorted(sizes) and sizes[1] > 0
+
+
+def test_a_call_takes_the_workspace_of_a_larger_batch():
+    """2,049 rows have two slices of the contraction and so more to hold than 4,096 with one; a call is refused
+    for less than its own."""
+    big = dict(rank=64, n_in=2560)
+    s = make_set(**big)
+    size = lambda T: _steps.lib().moe_adapters_bytes(ctypes.byref(s), T)
+    assert 0 < size(2049) <= size(4096)
+    assert adapters(big, tokens=2049, ldx=2560, nb=2 * 2049 * 64 * 4 - 1) == ESIZE
