@@ -117,15 +117,20 @@ def _rows(device: int, t, what: str, shape, written: bool = False):
 def _count(n: int, what: str) -> int:
     """n as the C call takes it: ctypes would cut a larger one to its low 32 bits."""
     if n > 0x7fffffff:
-        raise MoeError(-1, f"{what}: {n} rows")
+        raise MoeError(-1, f"{what}: a size of {n}")
     return n
+
+
+def _ints(*sizes: int) -> bool:
+    """Whether the C call can take the sizes of a query."""
+    return all(abs(n) <= 0x7fffffff for n in sizes)
 
 
 def _matrix(t, what: str):
     if t is None or t.dim() != 2:
         raise MoeError(-1, f"{what}: {None if t is None else tuple(t.shape)} is not a matrix")
     shape = t.shape
-    _count(shape[0], what)
+    _count(max(shape), what)
     return shape
 
 
@@ -156,7 +161,7 @@ def moe_route(logits, ids, w, renorm: bool = True, scale: float = 1.0, stream=No
 
 
 def moe_balance_bytes(tokens: int, n_expert: int, n_seq: int) -> int:
-    return int(lib().moe_balance_bytes(tokens, n_expert, n_seq))
+    return int(lib().moe_balance_bytes(tokens, n_expert, n_seq)) if _ints(tokens, n_expert, n_seq) else 0
 
 
 def moe_route_balance(logits, seq_off, coef: float, ids, w, counts, probs, loss, workspace,
@@ -240,6 +245,7 @@ class AdapterSet:
                                                                   for t in (a, b)))
         n, r, n_in = a.shape
         n_out = b.shape[1]
+        _count(max(n, r, n_in, n_out), "AdapterSet")
         code = _dtype(a, "a")
         if code == MOE_F32:
             raise MoeError(-3, f"a: {a.dtype}")
@@ -254,7 +260,7 @@ class AdapterSet:
 
 
 def moe_adapters_bytes(adapters: AdapterSet, tokens: int) -> int:
-    return int(lib().moe_adapters_bytes(adapters.ref, tokens))
+    return int(lib().moe_adapters_bytes(adapters.ref, tokens)) if _ints(tokens) else 0
 
 
 def moe_adapters(adapters: AdapterSet, ids, x, base, out, workspace, stream=None):

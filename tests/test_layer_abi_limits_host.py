@@ -2,8 +2,9 @@
 import ctypes
 
 import pytest
+import torch
 
-from quantized_moe_expert_scatter_amd import _steps
+from quantized_moe_expert_scatter_amd import _lib, _steps
 from tests.test_layer_abi_host import EINVAL, ESIZE, adapters, combine, make_set
 
 
@@ -37,3 +38,21 @@ def test_a_call_takes_the_workspace_of_a_larger_batch():
     size = lambda T: _steps.lib().moe_adapters_bytes(ctypes.byref(s), T)
     assert 0 < size(2049) <= size(4096)
     assert adapters(big, tokens=2049, ldx=2560, nb=2 * 2049 * 64 * 4 - 1) == ESIZE
+
+
+def test_binding_refuses_sizes_past_an_int():
+    """ctypes would cut them to their low 32 bits: columns, matrix sizes, and the size queries' arguments."""
+    far = (1 << 32) + 8
+    bf16 = dict(dtype=torch.bfloat16, device="meta")
+    with pytest.raises(_lib.MoeError, match=str(far)) as e:
+        _steps._matrix(torch.empty(1, far, device="meta"), "logits")
+    assert e.value.status == EINVAL
+    for a, b in (((far, 8, 8), (far, 8, 8)), ((1, far, 8), (1, 8, far)), ((1, 8, far), (1, 8, 8)),
+                 ((1, 8, 8), (1, far, 8))):
+        with pytest.raises(_lib.MoeError, match=str(far)) as e:
+            _steps.AdapterSet(torch.empty(a, **bf16), torch.empty(b, **bf16), torch.empty(a[0], device="meta"))
+        assert e.value.status == EINVAL
+    for args in ((far, 8, 1), (8, far, 1), (8, 8, far)):
+        assert _steps.moe_balance_bytes(*args) == 0
+    held = type("Set", (), {"ref": ctypes.byref(make_set())})
+    assert _steps.moe_adapters_bytes(held, 8) > 0 and _steps.moe_adapters_bytes(held, far) == 0
