@@ -45,6 +45,8 @@ class DeviceLayer:
                  seq_off: np.ndarray = None, balance_coef: float = 0.0, adapters=None,
                  adapter_ids: np.ndarray = None):
         import torch
+        if logits is not None and logits.shape != (x.shape[0], w_gu.n_expert):
+            raise ValueError(f"logits: shape {logits.shape}; {(x.shape[0], w_gu.n_expert)} wanted")
         self.device = torch.device(device)
         self.guard = (guard + 255) // 256 * 256
         self._guarded = {}

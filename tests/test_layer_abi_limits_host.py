@@ -1,10 +1,13 @@
-"""The C ABI of include/moe_layer.h on the host (no GPU), at its limits."""
+"""The C ABI of include/moe_layer.h at its limits, and what its binding and the layer refuse (no GPU)."""
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
 from quantized_moe_expert_scatter_amd import _lib, _steps
+from quantized_moe_expert_scatter_amd import workloads as wl
+from quantized_moe_expert_scatter_amd.layer import DeviceLayer
 from tests.test_layer_abi_host import EINVAL, ESIZE, adapters, combine, make_set
 
 
@@ -56,3 +59,11 @@ def test_binding_refuses_sizes_past_an_int():
         assert _steps.moe_balance_bytes(*args) == 0
     held = type("Set", (), {"ref": ctypes.byref(make_set())})
     assert _steps.moe_adapters_bytes(held, 8) > 0 and _steps.moe_adapters_bytes(held, far) == 0
+
+
+@pytest.mark.parametrize("shape", [(4, 9), (4, 7), (5, 8), (4, 8, 1)])
+def test_layer_refuses_logits_of_another_shape(shape):
+    """Experts that the layer does not have would be chosen, and their rows left out of the plan."""
+    L = wl.make_layer(wl.small_config("shape", 4, 128, 64, 8, 2, seed=1))
+    with pytest.raises(ValueError, match="logits"):
+        DeviceLayer(L.x, None, L.w_gu, L.w_down, logits=np.zeros(shape, np.float32), topk=2)
