@@ -76,3 +76,54 @@ def test_fp16_matrices_beside_fp32_values_lose_nothing(T, rank, where):
               x.cuda(), torch.zeros(T, n_out, device="cuda")).double().cpu()
     off = ((out - want) / want).abs().max().item() / ref.U
     assert off <= 2.0 * (1 + 2.0 ** -7), off
+
+
+def inputs(T, n, rank, dtype, wdtype, n_in=72, n_out=136, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    rand = lambda dt, *shape: torch.randn(*shape, generator=g).to(DT[dt]).cuda()
+    ids = (torch.arange(T, dtype=torch.int32) * n // T).cuda()
+    return dict(a=rand(wdtype, n, rank, n_in), b=rand(wdtype, n, n_out, rank), scale=torch.ones(n, device="cuda"),
+                ids=ids, x=rand(dtype, T, n_in), base=rand(dtype, T, n_out))
+
+
+@pytest.mark.parametrize("dtype,wdtype", TYPES)
+@pytest.mark.parametrize("T,rank", FORMS)
+def test_what_is_not_finite_stays_in_its_rows(T, rank, dtype, wdtype):
+    """NaN or an infinity in a row of x reaches that row, in a or b of an adapter its rows, and no others."""
+    print("not finite", T, rank, dtype, wdtype, flush=True)
+    d = inputs(T, 5, rank, dtype, wdtype)
+    clean = run(**d)
+    rows = [0, T // 2 + 1, T - 1]
+    d["x"][rows[0], 3], d["x"][rows[1], 0], d["x"][rows[2]] = float("nan"), float("inf"), float("-inf")
+    d["a"][1].fill_(float("nan"))
+    d["b"][3, :, 0] = float("inf")
+    got = run(**d)
+    touched = (d["ids"] == 1) | (d["ids"] == 3)
+    touched[rows] = True
+    assert torch.equal(got[~touched], clean[~touched])
+    assert not got[touched].isfinite().any()
+
+
+@pytest.mark.parametrize("dtype,wdtype", TYPES)
+@pytest.mark.parametrize("T,rank", FORMS)
+def test_what_lies_past_an_adapters_own_rank_is_not_read(T, rank, dtype, wdtype):
+    """Adapters of several ranks in a tile: NaN and infinities in the rows of a and columns of b past each
+    one's own give what zeros give, and ranks outside [0, rank] what the nearest one gives."""
+    print("own ranks", T, rank, dtype, wdtype, flush=True)
+    n = 6
+    d = inputs(T, n, rank, dtype, wdtype, seed=1)
+    d["ids"] = (torch.arange(T, dtype=torch.int32) % n).cuda()
+    own = [0, 1, rank - 3, rank // 2, rank, 5]
+    d["ranks"] = torch.tensor(own, dtype=torch.int32, device="cuda")
+    outs = []
+    for fill in (0.0, float("nan"), float("inf")):
+        for i, r in enumerate(own):
+            d["a"][i, r:] = fill
+            d["b"][i, :, r:] = fill
+        outs.append(run(**d))
+    d["ranks"][0], d["ranks"][4] = -2 ** 31, 2 ** 31 - 1
+    outs.append(run(**d))
+    assert outs[0].isfinite().all() and torch.equal(outs[0][::n], d["base"][::n])
+    for o in outs[1:]:
+        assert torch.equal(o, outs[0])
+    assert not torch.equal(outs[0][1::n], d["base"][1::n])

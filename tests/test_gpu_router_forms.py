@@ -53,3 +53,65 @@ def test_gradient_of_as_many_sequences_as_an_int_counts():
     want, size = ref.route_backward(l, ids, None, True, 1.0, [0, 10, 30], 2.0, mine)
     assert np.all(np.abs(d.cpu().numpy() - want) <= size * (rtol(E, 16.0) + 32 * ref.U))
     assert not d[30:].any() and d[:30].any(dim=1).all()
+
+
+# experts per lane 1, 1, 2, 8, 16, 32: a workgroup takes several rounds of rows above 512 times its
+# waves (16; 8 and 4 for the last two)
+@pytest.mark.parametrize("T,E,K", [(20011, 40, 3), (8193, 64, 8), (17000, 100, 6), (9000, 512, 10), (9001, 509, 3),
+                                   (5000, 1000, 16), (130, 1000, 16), (130, 100, 6), (3333, 2047, 12)])
+@pytest.mark.parametrize("bounds,dtype,kind", [("one", "f32", "normal"), ("ragged", "bf16", "closed"),
+                                               ("steps", "f32", "closed"), ("steps", "f16", "ties")])
+def test_balance_in_several_rounds(T, E, K, bounds, dtype, kind):
+    """Sequences that end anywhere in a workgroup's range, against the plain form."""
+    print("balance", T, E, K, bounds, dtype, kind, flush=True)
+    dev, l = make(T, E, dtype, seed=T, kind=kind)
+    off = sorted({5, *range(5, T - 9, 37 if T < 9000 else 211), T - 9}) if bounds == "steps" else offsets(T, bounds)
+    S = len(off) - 1
+    ids, w = torch.empty(T, K, dtype=torch.int32, device="cuda"), torch.empty(T, K, device="cuda")
+    counts = torch.full((S + 1, E), -5, dtype=torch.int32, device="cuda")
+    probs = torch.full((S + 1, E), -5.0, device="cuda")
+    loss = torch.full((2,), -5.0, device="cuda")
+    nb = moe.moe_balance_bytes(T, E, S)
+    ws = torch.full((nb + 64,), 0xA5, dtype=torch.uint8, device="cuda")
+    moe.moe_route_balance(dev, torch.tensor(off, dtype=torch.int32, device="cuda"), 0.3, ids, w, counts[:S],
+                          probs[:S], loss[:1], ws[:nb], renorm=False, scale=1.5)
+    torch.cuda.synchronize()
+    assert (ws[nb:] == 0xA5).all() and (counts[S:] == -5).all() and (probs[S:] == -5.0).all() and loss[1] == -5.0
+    want_ids, want_w = ref.route(l, K, False, 1.5)
+    assert np.array_equal(ids.cpu().numpy(), want_ids)
+    assert np.all(np.abs(w.cpu().numpy() - want_w)
+                  <= want_w * (rtol(E) + (spread_of(l, want_ids) + K) * ref.U) + 1.5 * 2.0 ** -148)
+    want_c, want_p, want_l = ref.balance(l, want_ids, off, 0.3)
+    assert np.array_equal(counts[:S].cpu().numpy(), want_c)
+    # a range holds at most T / 512 rows rounded up to the waves, dealt to them, and then at most 16 waves are added
+    chain = max(16, (T // 512 // 16 + 1) * 16) / 4 + 16
+    assert np.all(np.abs(probs[:S].cpu().numpy() - want_p) <= want_p * (rtol(E) + (chain + 2) * ref.U) + 0.5 * ref.U)
+    # a probability's 0.5 u enters times coef / S * counts * E / (K n)
+    share = sum(want_c[s].sum() * E / (K * max(off[s + 1] - off[s], 1)) for s in range(S))
+    assert abs(float(loss[0]) - want_l) <= want_l * (rtol(E) + (chain + 16) * ref.U) + 0.3 / S * share * 0.5 * ref.U
+
+
+@pytest.mark.parametrize("T,E,K", [(65537, 8, 2), (70001, 60, 3), (66000, 130, 2)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_more_rows_than_waves(T, E, K, dtype):
+    """Above 65,536 rows the router's and the gradient's waves take several."""
+    print("route", T, E, K, dtype, flush=True)
+    dev, l = make(T, E, dtype, seed=E)
+    ids, w = run_route(dev, K, True, 1.0)
+    want_ids, want = ref.route(l, K, True)
+    assert np.array_equal(ids, want_ids)
+    assert np.all(np.abs(w - want) <= want * (rtol(E) + (spread_of(l, want_ids) + K) * ref.U) + 2.0 ** -148)
+    rng = np.random.default_rng(T)
+    dw = rng.standard_normal((T, K)).astype(np.float32)
+    off = [0, T // 2, T - 5]
+    counts, _, _ = ref.balance(l, ids, off, 1.0)
+    out = torch.full((T + 1, E), 9.0, dtype=dev.dtype, device="cuda")
+    moe.moe_route_backward(dev, torch.from_numpy(ids).cuda(), torch.from_numpy(dw).cuda(), out[:T], renorm=False,
+                           seq_off=torch.tensor(off, dtype=torch.int32, device="cuda"), coef=0.3,
+                           counts=torch.from_numpy(counts.astype(np.int32)).cuda())
+    torch.cuda.synchronize()
+    d, size = ref.route_backward(l, ids, dw.astype(np.float64), False, 1.0, off, 0.3, counts)
+    spread = (l.max(axis=1) - l.min(axis=1)).max()
+    tol = size * (rtol(E) + (K + 16 + 2 * spread) * ref.U) + np.abs(d) * ref.HALF[dtype] + 2.0 ** -133
+    assert np.all(np.abs(out[:T].double().cpu().numpy() - d) <= tol)
+    assert (out[T:] == 9.0).all()
