@@ -129,8 +129,9 @@ def _ints(*sizes: int) -> bool:
 def _matrix(t, what: str):
     if t is None or t.dim() != 2:
         raise MoeError(-1, f"{what}: {None if t is None else tuple(t.shape)} is not a matrix")
-    shape = t.shape
-    _count(max(shape), what)
+    rows, cols = shape = t.shape
+    if rows > 0x7fffffff or cols > 0x7fffffff:
+        _count(max(shape), what)
     return shape
 
 
