@@ -18,11 +18,19 @@ namespace {
 
 constexpr int kThreads = 256;
 // The single launch computes a row's h in each of its output slices, so it is
-// taken while tokens * rank * slices is small.  Measured at 2560 -> 2560 (3
-// slices), rows of one adapter / of 48 in any order: rank 16, 256 rows 9.3 /
-// 12.4 us in one launch, 257 rows 9.2 / 20.1 in two; rank 32, 128 rows 9.7 /
-// 14.0 in one, 200 rows 9.7 / 20.8 in two; rank 64, 64 rows 10.8 / 16.6 in one,
-// 128 rows 20.5 / 29.0 in one and 10.8 / 23.8 in two.
+// taken while tokens * rank * slices is small.  Measured with fp32 rows, one
+// launch / two, 2560 -> 2560 (3 slices):
+//               one adapter                         48 adapters in any order
+//   rank  16    1 row 4.4 / 8.3, 128 7.1 / 9.2      16 rows 4.7 / 22.6, 128 8.4 / 17.3
+//   rank  32    1 row 5.8 / 8.6, 128 10.0 / 9.6     16 rows 6.1 / 20.5, 128 14.8 / 18.1
+//   rank  64    1 row 10.3 / 9.8, 64 11.3 / 10.8    16 rows 10.7 / 29.0, 64 16.6 / 25.6
+//   rank 128    1 row 17.3 / 12.3, 16 17.8 / 13.3   16 rows 24.6 / 41.9
+//   rank 256    1 row 28.6 / 16.9, 16 30.2 / 18.1   16 rows 42.0 / 66.0
+// and past the rule: rank 16, 256 rows in one and 257 in two 9.3 / 9.2 and 12.4 /
+// 20.1, rank 64, 128 rows 20.5 / 10.8 and 29.0 / 23.8.
+// The rule does not weigh n_in, and is not the best of both where few rows of
+// one adapter meet a high rank or a long contraction (n_in 16384: rank 16 1 row
+// 14.1 / 11.8, 16 rows in any order 15.0 / 36.3; rank 256 132 / 22 and 139 / 86).
 constexpr int kFewRows = 256;
 constexpr int kFewValues = 12288;
 
@@ -480,12 +488,13 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterArgs g, A
 // its columns rows of the tile, and a pass's results are taken from the columns
 // whose rows have its adapter.  The 16 x 64 results pass through LDS so that
 // base and out move in whole row segments: 256 bytes of a row per 16 lanes
-// reach 6.2 TB/s in a copy of this shape, the 64 that the matrix unit's layout
-// gives 4.6.  KB: blocks of 32 rank values whose part of b is held in registers
+// reach 6.2 TB/s in a copy of 16,384 fp32 rows of 2560 past the caches, the 64
+// that the matrix unit's layout gives 4.6.  KB: blocks of 32 rank values whose part of b is held in registers
 // (0: any rank, 64 values at a time).
-//   2,047 fp16 rows of 2560 at rank 24: 10.5 us for 21 MB.  Loading the first
-// part of b with base and h, or all planes of h at once, was slower (11.6-12.3),
-// b turned through LDS as in the other kernel level (11.1).
+//   2,047 fp16 rows of 2560 at rank 24: 10.8 us for 21 MB.  Loading the first
+// part of b with base and h, or all planes of h at once, was slower, b turned
+// through LDS as in the other kernel level (11.6-12.3 and 11.1 where this took
+// 10.5, with two parts of h).
 constexpr int kUpRank = 64;          // rank values of h in LDS at a time
 constexpr int kUpStride = kUpRank + 4;
 // Parts of h: all of its fp32, for 16-bit rows too, where the third shows only if
@@ -663,7 +672,7 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterArgs g, Ada
 //   Bound by base and out: 16,384 fp32 rows of 2560 at rank 64 take 69 us (336
 // MB, 4.9 TB/s; the 16-row kernel 89, 32 rows of it 73).  Short stretches of
 // outputs are best, 1,024 / 2,048 / 4,096 / 10,240 workgroups 84 / 71 / 69 / 79
-// us.  2,047 fp16 rows at rank 24 take 12.9 us against the 16-row kernel's 10.6.
+// us.  2,047 fp16 rows at rank 24 take 12.4 us against the 16-row kernel's 10.8.
 constexpr int kWideGroups = 4096;
 
 template <int XT, int WT, int KB>

@@ -16,8 +16,8 @@
 // gradient against each of its K rows (the routing weights' gradient), and
 // times each weight (the rows' gradient).  It is bound by HBM too: K + 1 rows
 // read per token, K written.  2,048 tokens, top-10 of 2560: 231 MB in 35 us
-// (6.5 TB/s); 8,192 with the rows' gradient: 1,762 MB in 319 us (5.5 TB/s,
-// what a large copy reaches).
+// (6.5 TB/s); 8,192 with the rows' gradient: 1,762 MB in 315 us (5.6 TB/s;
+// torch's copy of 1 GB reaches 5.3).
 #include "internal.h"
 #include "layer_ops.h"
 #include "wave.cuh"
