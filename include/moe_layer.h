@@ -162,8 +162,9 @@ size_t moe_adapters_bytes(const moe_adapter_set *set, int tokens);
  *          aligned, free again when the call's work has run
  * a * x is held in fp32, the result rounded once.  What a row holds reaches no
  * other row; an infinity in x, a, b or a * x may give NaN where the formula has
- * an infinity.  A row's result does not depend on the rows beside it; its last
- * bits may on how many there are, by the order of its sums. */
+ * an infinity, and products below 2^-126 (also of the low bits of a value below
+ * 2^-110) may count as 0.  A row's result does not depend on the rows beside it;
+ * its last bits may on how many there are, by the order of its sums. */
 int moe_adapters(const moe_adapter_set *set, const int32_t *ids, int tokens, int dtype,
                  const void *x, int64_t ldx, const void *base, int64_t ldb, void *out, int64_t ldo,
                  void *workspace, size_t workspace_bytes, void *stream);

@@ -127,3 +127,25 @@ def test_what_lies_past_an_adapters_own_rank_is_not_read(T, rank, dtype, wdtype)
     for o in outs[1:]:
         assert torch.equal(o, outs[0])
     assert not torch.equal(outs[0][1::n], d["base"][1::n])
+
+
+@pytest.mark.parametrize("T,rank", [(8, 16)] + FORMS)
+@pytest.mark.parametrize("wdtype", ["bf16", "f16"])
+@pytest.mark.parametrize("e", [-112, -118, -126])
+def test_tiny_values_lose_no_more_than_the_smallest_normal_number(T, rank, wdtype, e):
+    """A product below 2^-126 may count as 0, and so may a part of a value: at most six products of two
+    parts for each of the formula's, of factors below 4 and 2^-126, so 2^-126 * 6 * 4 a term of a * x, and as
+    much a term of b * h."""
+    print("tiny", T, rank, wdtype, e, flush=True)
+    n_in, n_out = 64, 72
+    g = torch.Generator().manual_seed(2)
+    rand = lambda *shape: torch.rand(*shape, generator=g) * 2 - 1
+    a, b = rand(1, rank, n_in).to(DT[wdtype]), rand(1, n_out, rank).to(DT[wdtype])
+    x = rand(T, n_in) * 2.0 ** e
+    out = run(a.cuda(), b.cuda(), torch.ones(1, device="cuda"), torch.zeros(T, dtype=torch.int32, device="cuda"),
+              x.cuda(), torch.zeros(T, n_out, device="cuda")).double().cpu()
+    A, B, X = a[0].double(), b[0].double(), x.double()
+    want = X @ A.t() @ B.t()
+    size = X.abs() @ A.abs().t() @ B.abs().t()
+    lost = 2.0 ** -126 * 24 * (n_in * B.abs().sum(dim=1) + rank)
+    assert bool(((out - want).abs() <= size * (n_in + rank + 8) * ref.U + lost).all())
