@@ -115,3 +115,31 @@ def test_more_rows_than_waves(T, E, K, dtype):
     tol = size * (rtol(E) + (K + 16 + 2 * spread) * ref.U) + np.abs(d) * ref.HALF[dtype] + 2.0 ** -133
     assert np.all(np.abs(out[:T].double().cpu().numpy() - d) <= tol)
     assert (out[T:] == 9.0).all()
+
+
+@pytest.mark.parametrize("E", [60, 512, 1000])
+def test_padding_that_is_not_a_number_joins_nothing(E):
+    """NaN and infinities in rows outside the sequences leave the statistics and the other rows' gradient alone."""
+    T, K, off = 700, 4, [9, 300, 650]
+    dev, _ = make(T, E, "f32", seed=E)
+    inside = torch.zeros(T, dtype=torch.bool)
+    inside[off[0]:off[-1]] = True
+    inside = inside.cuda()
+    outs = []
+    for fill in (0.0, float("nan"), float("inf")):
+        l = dev.clone()
+        l[~inside] = fill
+        ids, w = torch.empty(T, K, dtype=torch.int32, device="cuda"), torch.empty(T, K, device="cuda")
+        counts = torch.empty(2, E, dtype=torch.int32, device="cuda")
+        probs, loss = torch.empty(2, E, device="cuda"), torch.empty(1, device="cuda")
+        so = torch.tensor(off, dtype=torch.int32, device="cuda")
+        ws = torch.full((moe.moe_balance_bytes(T, E, 2),), 0xFF, dtype=torch.uint8, device="cuda")
+        moe.moe_route_balance(l, so, 0.3, ids, w, counts, probs, loss, ws)
+        dw = torch.ones_like(w)
+        dw[~inside] = fill
+        d = torch.empty_like(l)
+        moe.moe_route_backward(l, ids, dw, d, seq_off=so, coef=0.3, counts=counts)
+        outs.append((counts, probs, loss, ids[inside], w[inside], d[inside]))
+    for o in outs[1:]:
+        for a, b in zip(o, outs[0]):
+            assert torch.equal(a, b)
